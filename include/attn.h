@@ -252,7 +252,9 @@ int attn_debug_inject(int mode);
  *   kind 0 forward, 1 backward pre-pass (D, padded lse, dQ clear),
  *   kind 2 backward main kernel, 3 backward dQ conversion,
  *   kind 4 decoding step (per key chunk), 5 decoding merge of the chunks,
- *   kind 6 projection GEMM (attn_qkv_projection, attn_out_projection and their _bwd).
+ *   kind 6 projection GEMM (attn_qkv_projection, attn_out_projection and their _bwd),
+ *   kind 7 norm + rotation, 8 cache write and read, 9 tree decoding step (per
+ *   key split), 10 its joining of the splits.
  * launches / total_ms may be NULL. Returns ATTN_OK, ATTN_ERR_INVALID_ARG for an
  * unknown kind, or ATTN_ERR_CUDA. Enabling costs two event records per launch.
  */
@@ -349,6 +351,100 @@ size_t attn_decode_workspace_bytes(int B, int h, int n, int m, int d_k, int d_v)
 int attn_decode(const void* q, const void* k, const void* v, void* o, float* lse, const int* kv_len,
                 int B, int h, int n, int m, int d_k, int d_v, float scale, void* workspace,
                 size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * Per-head RMS norm of queries and keys and the rotation by their positions,
+ * in one pass between attn_qkv_projection and the attention:
+ *   r = (mean_c x_c^2 + eps)^(-1/2),  y_c = x_c r w_c,
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_a sin t + y_b cos t)
+ * for each pair of the head's first `rot` columns (the others stay y). Pair i
+ * is columns (i, i + rot/2), or (2i, 2i + 1) with `interleaved`; its angle is
+ * t = positions[axis(i)] * freqs[i], taken exactly (far positions lose nothing).
+ *   q, q_out [B, h, n, d], k, k_out [B, h_kv, n, d]  bf16; an output may be its input
+ *   w_q, w_k  [d] bf16      positions [axes, B, n] int32      freqs [rot/2] fp32, |f| < 2^24
+ *   sections  HOST array of `axes` counts that sum to rot/2: the first sections[0]
+ *             pairs turn by positions[0], the next by positions[1], ... (images and
+ *             video: time, height, width); may be NULL with axes = 1
+ * d in {32, 64, 128}, rot a multiple of 16 in [0, d], axes 1 to 3, eps > 0.
+ * h or h_kv may be 0 (that side's pointers are then ignored). With rot = 0
+ * positions and freqs may be NULL (the norm alone).
+ *
+ * attn_qk_norm_rope_bwd: with u the upstream gradient (dq_out, dk_out) turned by -t,
+ *   dx = r (w u - x r mean_c(w u x r)),  dw_c = sum over all rows of u_c x_c r
+ *   q, k: the inputs of the forward; dq, dk (bf16; either may be its upstream
+ *   gradient); dw_q, dw_k [d] bf16. Sums are fp32, in an order that the sizes alone fix.
+ *   workspace: attn_qk_norm_rope_bwd_workspace_bytes(...) bytes, 16-byte aligned.
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG (null or misaligned pointer, negative
+ * size, sections that do not sum to rot/2, eps <= 0, short workspace),
+ * ATTN_ERR_UNSUPPORTED (other d, rot or axes; h + h_kv > 65535) or ATTN_ERR_CUDA.
+ * No rows: ATTN_OK (the backward clears dw). Asynchronous on `stream`; profiling kind 7.
+ */
+int attn_qk_norm_rope(const void* q, const void* k, const void* w_q, const void* w_k, const int* positions,
+                      const float* freqs, void* q_out, void* k_out, int B, int h, int h_kv, int n, int d, int rot,
+                      int axes, const int* sections, int interleaved, float eps, attn_stream_t stream);
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int B, int h, int h_kv, int n, int d);
+int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* w_q, const void* w_k, const int* positions,
+                          const float* freqs, const void* dq_out, const void* dk_out, void* dq, void* dk, void* dw_q,
+                          void* dw_k, int B, int h, int h_kv, int n, int d, int rot, int axes, const int* sections,
+                          int interleaved, float eps, void* workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * Key/value caches [B, h_kv, m, d]: bf16, or quantised. A quantised row (a
+ * position of a head) is d e4m3 codes and one byte e + 127: e is the least
+ * integer with max|x| <= 448 2^e over the row's finite values, kept in
+ * [-117, 119] (0 for a row of zeros), code = x 2^-e rounded to e4m3 (nearest
+ * even, saturating; infinities saturate, NaN stays NaN), value = code 2^e.
+ * Codes are one byte each; k_exp, v_exp [B, h_kv, m] hold the exponent bytes.
+ *
+ * attn_cache_write: the new rows k, v [B, h_kv, n, d] (bf16) of each sequence into
+ *   the caches. kv_len[b] is the sequence's length after the write (as the
+ *   decoding calls take it), new_len[b] the number of its new rows: row
+ *   i < new_len[b] goes to position kv_len[b] - new_len[b] + i. Rows at or past
+ *   new_len[b] are padding; positions before 0 are dropped; every other cache
+ *   position stays as it was. kv_len NULL: m; new_len NULL: n; both are
+ *   clamped to [0, m] and [0, n]. With k_exp and v_exp NULL the caches are
+ *   bf16 and the rows are copied.
+ * attn_cache_read: a quantised cache back to bf16 k, v [B, h_kv, m, d], exactly
+ *   (every value is a bf16 number); rows at or past kv_len[b] (NULL: m) become
+ *   zeros, so attn_fwd_varlen can take the result.
+ * Tensors 16-byte aligned, lengths int32 device arrays; d in {32, 64, 128}.
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED (other d, more
+ * than 2^34 rows) or ATTN_ERR_CUDA. Asynchronous on `stream`; profiling kind 8.
+ */
+int attn_cache_write(const void* k, const void* v, void* k_cache, void* v_cache, void* k_exp, void* v_exp,
+                     const int* kv_len, const int* new_len, int B, int h_kv, int n, int m, int d,
+                     attn_stream_t stream);
+int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_exp, const void* v_exp, void* k, void* v,
+                    const int* kv_len, int B, int h_kv, int m, int d, attn_stream_t stream);
+
+/*
+ * Attention of the n newest positions of each sequence, drafted as a tree,
+ * over its cache (and, with n = 1, the decoding step of a quantised cache or
+ * of shared key heads). Sequence b has L_b = kv_len[b] cached positions
+ * (NULL: m; clamped to [0, m]), its n newest among them already written. Query
+ * i sees every position before L_b - n, and position L_b - n + t where bit t of
+ * tree[b][i] is set (its ancestors and itself); tree NULL: t <= i. A query
+ * that sees nothing is the empty sum: O = 0, lse = -inf. What the cache holds in
+ * positions that a query does not see never reaches its result, NaN and
+ * infinities included.
+ *   q, o [B, h, n, d] bf16, 1 <= n <= 64; query head i uses key head i / (h / h_kv)
+ *   k, v [B, h_kv, m, d]: bf16 with k_exp and v_exp NULL, else the codes and bytes
+ *        of attn_cache_write
+ *   lse  [B, h, n] fp32 or NULL      tree [B, n] 64-bit words, device, 8-byte aligned, or NULL
+ *   workspace: attn_decode_tree_workspace_bytes(...) bytes, 16-byte aligned (may
+ *        be NULL when that is 0; every byte read is written first; not shared by
+ *        calls that can overlap)
+ * Scores, sums and O accumulate in fp32; the weights are rounded to bf16 for
+ * the product with V. d in {32, 64, 128}, h a multiple of h_kv.
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG (null or misaligned pointer, n outside
+ * [1, 64], m < 1, h not a multiple of h_kv, short workspace, non-finite scale),
+ * ATTN_ERR_UNSUPPORTED (other d, B h_kv > 65535, h n >= 2^20) or ATTN_ERR_CUDA.
+ * Asynchronous on `stream`; profiling kinds 9 (step) and 10 (joining the key splits).
+ */
+size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int m, int d);
+int attn_decode_tree(const void* q, const void* k, const void* v, void* o, float* lse, const void* k_exp,
+                     const void* v_exp, const int* kv_len, const long long* tree, int B, int h, int h_kv, int n, int m,
+                     int d, float scale, void* workspace, size_t workspace_bytes, attn_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -30,6 +30,8 @@ __all__ = [
     "attn_qkv_projection", "attn_out_projection", "attn_qkv_projection_bwd", "attn_out_projection_bwd",
     "attn_qkv_projection_bwd_workspace_bytes", "attn_out_projection_bwd_workspace_bytes",
     "attn_fwd_bwd_host", "HostStepBuffers", "EXPORTED_SYMBOLS", "KERNEL_KINDS",
+    "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_bwd_workspace_bytes",
+    "attn_cache_write", "attn_cache_read", "attn_decode_tree", "attn_decode_tree_workspace_bytes",
 ]
 # attn_fwd / attn_bwd take an optional ``kv_len`` (int32 CUDA tensor [B]: real
 # keys per sequence) and an optional ``window`` = (left, right) (restricted
@@ -51,10 +53,13 @@ EXPORTED_SYMBOLS = (
     "attn_qkv_projection", "attn_out_projection", "attn_qkv_projection_bwd_workspace_bytes",
     "attn_qkv_projection_bwd", "attn_out_projection_bwd_workspace_bytes", "attn_out_projection_bwd",
     "attn_fwd_bwd_host",
+    "attn_qk_norm_rope", "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_bwd",
+    "attn_cache_write", "attn_cache_read", "attn_decode_tree_workspace_bytes", "attn_decode_tree",
 )
 
 # Kernel kinds of attn_profile_read.
-KERNEL_KINDS = {"fwd": 0, "bwd_pre": 1, "bwd_main": 2, "bwd_post": 3, "decode": 4, "decode_merge": 5, "proj": 6}
+KERNEL_KINDS = {"fwd": 0, "bwd_pre": 1, "bwd_main": 2, "bwd_post": 3, "decode": 4, "decode_merge": 5, "proj": 6,
+                "norm_rope": 7, "cache": 8, "tree": 9, "tree_merge": 10}
 
 _lock = threading.Lock()
 _lib = None
@@ -136,6 +141,20 @@ def load_library():
         lib.attn_profile_enable.restype = I
         lib.attn_profile_read.argtypes = [I, ctypes.POINTER(I), ctypes.POINTER(ctypes.c_double)]
         lib.attn_profile_read.restype = I
+        lib.attn_qk_norm_rope.argtypes = [vp] * 8 + [I] * 7 + [vp, I, F, vp]
+        lib.attn_qk_norm_rope.restype = I
+        lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [I] * 5
+        lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = SZ
+        lib.attn_qk_norm_rope_bwd.argtypes = [vp] * 12 + [I] * 7 + [vp, I, F, vp, SZ, vp]
+        lib.attn_qk_norm_rope_bwd.restype = I
+        lib.attn_cache_write.argtypes = [vp] * 8 + [I] * 5 + [vp]
+        lib.attn_cache_write.restype = I
+        lib.attn_cache_read.argtypes = [vp] * 7 + [I] * 4 + [vp]
+        lib.attn_cache_read.restype = I
+        lib.attn_decode_tree_workspace_bytes.argtypes = [I] * 6
+        lib.attn_decode_tree_workspace_bytes.restype = SZ
+        lib.attn_decode_tree.argtypes = [vp] * 9 + [I] * 6 + [F, vp, SZ, vp]
+        lib.attn_decode_tree.restype = I
         _lib = lib
         return lib
 
@@ -595,3 +614,237 @@ def attn_bwd_noalloc(q, k, v, o, lse, dO, causal: bool = False, scale: Optional[
     if st != ATTN_OK:
         raise AttnError(st, "attn_bwd_noalloc")
     return dq, dk, dv
+
+
+def _operand(name, t, shape, dtype, device):
+    """Checks one tensor of the calls below and returns its address (None for None)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _first(name, t, dims, dtype):
+    """The tensor that gives a call its sizes and its device."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    _operand(name, t, t.shape, dtype, t.device)
+    return t.device
+
+
+def _workspace(t, need, device):
+    import torch
+    if t is None:
+        t = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    elif not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return t, t.numel() * t.element_size()
+
+
+def _launch(fn, where, device, stream, *args):
+    """Calls fn(*args, stream) with the tensors' device current; raises on a status."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError(st, where)
+
+
+def _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections):
+    """Sizes, addresses and sections shared by attn_qk_norm_rope and its backward."""
+    import torch
+    bf = torch.bfloat16
+    first = k if q is None else q
+    dev = _first("k" if q is None else "q", first, 4, bf)
+    B, h, n, d = first.shape
+    h_kv = 0 if k is None else int(k.shape[1]) if k.dim() == 4 else -1
+    if q is None:
+        h = 0
+    ptrs = [None if q is None else q.data_ptr(),
+            None if k is None else _operand("k", k, (B, h_kv, n, d), bf, dev),
+            None if q is None else _operand("w_q", w_q, (d,), bf, dev),
+            None if k is None else _operand("w_k", w_k, (d,), bf, dev)]
+    rot, axes = 0, 1
+    pos = frq = None
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError("freqs must have one dimension")
+        rot = 2 * freqs.shape[0]
+        frq = _operand("freqs", freqs, freqs.shape, torch.float32, dev)
+        axes = positions.shape[0] if positions.dim() == 3 else 1
+        pos = _operand("positions", positions, (axes, B, n) if positions.dim() == 3 else (B, n), torch.int32, dev)
+    if sections is None:
+        sec = None
+        if axes > 1:
+            raise ValueError("positions of several axes need sections")
+    else:
+        if len(sections) != axes:
+            raise ValueError(f"{len(sections)} sections for positions of {axes} axes")
+        sec = (ctypes.c_int * axes)(*sections)
+    return dev, (B, h, h_kv, n, d, rot, axes, sec), ptrs + [pos, frq]
+
+
+def attn_qk_norm_rope(q, k, w_q, w_k, positions=None, freqs=None, sections=None, interleaved: bool = False,
+                      eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [B, h, n, d] and k [B, h_kv, n, d] with the weights
+    w_q, w_k [d] (bf16), and the rotation of their first 2 len(freqs) columns.
+
+    positions: int32 [B, n], or [axes, B, n] with ``sections`` (pairs per axis: time,
+    height, width); freqs: fp32, the angle of pair i is positions * freqs[i]. Pairs are
+    columns (i, i + len(freqs)), or neighbours with ``interleaved``. Without freqs: the
+    norm alone. q or k (with its weight) may be None. q_out may be q, k_out may be k.
+    Returns (q_out, k_out)."""
+    import torch
+    dev, (B, h, h_kv, n, d, rot, axes, sec), ptrs = _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections)
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+    po = None if q is None else _operand("q_out", q_out, q.shape, torch.bfloat16, dev)
+    ko = None if k is None else _operand("k_out", k_out, k.shape, torch.bfloat16, dev)
+    _launch(load_library().attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, *ptrs, po, ko, B, h, h_kv, n, d, rot,
+            axes, sec, 1 if interleaved else 0, eps)
+    return q_out, k_out
+
+
+def attn_qk_norm_rope_bwd_workspace_bytes(B, h, h_kv, n, d) -> int:
+    return int(load_library().attn_qk_norm_rope_bwd_workspace_bytes(B, h, h_kv, n, d))
+
+
+def attn_qk_norm_rope_bwd(q, k, w_q, w_k, positions, freqs, dq_out, dk_out, sections=None, interleaved: bool = False,
+                          eps: float = 1e-6, dq=None, dk=None, dw_q=None, dw_k=None, workspace=None, stream=None):
+    """Gradients of attn_qk_norm_rope from those of its results (dq_out, dk_out, e.g. of
+    attn_bwd); the other arguments as in the forward. dq may be dq_out, dk may be dk_out.
+    Returns (dq, dk, dw_q, dw_k)."""
+    import torch
+    bf = torch.bfloat16
+    dev, (B, h, h_kv, n, d, rot, axes, sec), ptrs = _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections)
+    up, out, dws = [], [], []
+    if q is not None:
+        dq = torch.empty_like(q) if dq is None else dq
+        dw_q = torch.empty_like(w_q) if dw_q is None else dw_q
+    if k is not None:
+        dk = torch.empty_like(k) if dk is None else dk
+        dw_k = torch.empty_like(w_k) if dw_k is None else dw_k
+    for name, x, g, dx, dw in (("q", q, dq_out, dq, dw_q), ("k", k, dk_out, dk, dw_k)):
+        up.append(None if x is None else _operand(f"d{name}_out", g, x.shape, bf, dev))
+        out.append(None if x is None else _operand(f"d{name}", dx, x.shape, bf, dev))
+        dws.append(None if x is None else _operand(f"dw_{name}", dw, (d,), bf, dev))
+    lib = load_library()
+    need = 0 if workspace is not None else lib.attn_qk_norm_rope_bwd_workspace_bytes(B, h, h_kv, n, d)
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    _launch(lib.attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream, *ptrs, *up, *out, *dws, B, h, h_kv, n, d,
+            rot, axes, sec, 1 if interleaved else 0, eps, workspace.data_ptr(), ws_bytes)
+    return dq, dk, dw_q, dw_k
+
+
+def _cache_args(k_cache, v_cache, k_exp, v_exp):
+    """Device, sizes and addresses of a cache: bf16, or e4m3 codes with exponent bytes."""
+    import torch
+    dtype = torch.bfloat16 if k_exp is None else torch.float8_e4m3fn
+    dev = _first("k cache", k_cache, 4, dtype)
+    B, h_kv, m, d = k_cache.shape
+    v = _operand("v cache", v_cache, k_cache.shape, dtype, dev)
+    if k_exp is None:
+        if v_exp is not None:
+            raise ValueError("k_exp and v_exp go together")
+        return dev, (B, h_kv, m, d), (k_cache.data_ptr(), v, None, None)
+    return dev, (B, h_kv, m, d), (k_cache.data_ptr(), v, _operand("k_exp", k_exp, (B, h_kv, m), torch.uint8, dev),
+                                  _operand("v_exp", v_exp, (B, h_kv, m), torch.uint8, dev))
+
+
+def attn_cache_write(k, v, k_cache, v_cache, kv_len=None, new_len=None, k_exp=None, v_exp=None, stream=None):
+    """Writes the new rows k, v [B, h_kv, n, d] (bf16) into the caches [B, h_kv, m, d].
+
+    kv_len (int32 CUDA [B], default m): lengths after the write; new_len (default n): real
+    new rows of each sequence, which go to positions kv_len - new_len ... kv_len - 1. With
+    k_exp, v_exp (uint8 [B, h_kv, m]) the caches are torch.float8_e4m3fn and the rows are
+    quantised as they are written; without, the caches are bf16. Everything else in the
+    caches stays as it was. Returns (k_cache, v_cache)."""
+    import torch
+    dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k_cache, v_cache, k_exp, v_exp)
+    if k.dim() != 4:
+        raise ValueError("k, v must be [B, h_kv, n, d]")
+    n = k.shape[2]
+    pk = _operand("k", k, (B, h_kv, n, d), torch.bfloat16, dev)
+    pv = _operand("v", v, (B, h_kv, n, d), torch.bfloat16, dev)
+    lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
+    new = None if new_len is None else _operand("new_len", new_len, (B,), torch.int32, dev)
+    _launch(load_library().attn_cache_write, "attn_cache_write", dev, stream, pk, pv, kc, vc, ke, ve, lens, new, B,
+            h_kv, n, m, d)
+    return k_cache, v_cache
+
+
+def attn_cache_read(k_cache, v_cache, k_exp, v_exp, kv_len=None, k=None, v=None, stream=None):
+    """A quantised cache (attn_cache_write) back as bf16 k, v [B, h_kv, m, d], exactly; rows
+    at or past kv_len (int32 CUDA [B], default m) are zeros. Returns (k, v)."""
+    import torch
+    if k_exp is None:
+        raise ValueError("attn_cache_read takes a quantised cache: k_exp and v_exp are needed")
+    dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k_cache, v_cache, k_exp, v_exp)
+    k = torch.empty(k_cache.shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(k_cache.shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    pk = _operand("k", k, k_cache.shape, torch.bfloat16, dev)
+    pv = _operand("v", v, k_cache.shape, torch.bfloat16, dev)
+    lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
+    _launch(load_library().attn_cache_read, "attn_cache_read", dev, stream, kc, vc, ke, ve, pk, pv, lens, B, h_kv, m,
+            d)
+    return k, v
+
+
+def attn_decode_tree_workspace_bytes(B, h, h_kv, n, m, d) -> int:
+    return int(load_library().attn_decode_tree_workspace_bytes(B, h, h_kv, n, m, d))
+
+
+def attn_decode_tree(q, k, v, kv_len=None, tree=None, k_exp=None, v_exp=None, scale: Optional[float] = None, out=None,
+                     lse=None, need_lse: bool = True, workspace=None, stream=None):
+    """The n <= 64 newest positions q [B, h, n, d] of each sequence over the caches k, v
+    [B, h_kv, m, d] (bf16, or torch.float8_e4m3fn with k_exp, v_exp), which hold their keys
+    and values already. Query head i uses key head i // (h / h_kv).
+
+    kv_len (int32 CUDA [B], default m): cached positions L. Query i sees the positions
+    before L - n, and position L - n + t where bit t of tree[b, i] (int64 CUDA [B, n]) is
+    set; without tree where t <= i. A query that sees nothing gives O = 0, lse = -inf.
+    Returns (O, lse)."""
+    import torch
+    bf = torch.bfloat16
+    dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k, v, k_exp, v_exp)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, h, n, d]")
+    h, n = q.shape[1], q.shape[2]
+    pq = _operand("q", q, (B, h, n, d), bf, dev)
+    lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
+    words = None if tree is None else _operand("tree", tree, (B, n), torch.int64, dev)
+    out = torch.empty_like(q) if out is None else out
+    po = _operand("out", out, q.shape, bf, dev)
+    if need_lse and lse is None:
+        lse = torch.empty((B, h, n), dtype=torch.float32, device=dev)
+    pl = None if lse is None else _operand("lse", lse, (B, h, n), torch.float32, dev)
+    lib = load_library()
+    need = 0 if workspace is not None else lib.attn_decode_tree_workspace_bytes(B, h, h_kv, n, m, d)
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    _launch(lib.attn_decode_tree, "attn_decode_tree", dev, stream, pq, kc, vc, po, pl, ke, ve, lens, words, B, h, h_kv,
+            n, m, d, 1.0 / math.sqrt(d) if scale is None else float(scale), workspace.data_ptr(), ws_bytes)
+    return out, lse

@@ -102,6 +102,24 @@ bool make_map3(CUtensorMap* map, const void* base, long long d0, long long d1, l
   return r == CUDA_SUCCESS;
 }
 
+// 3-D map over a [BH, S, d] array of 8-bit codes: box = (d, box_rows, 1 head),
+// swizzled over the row's d bytes (d = 32: not).
+bool make_code_map(CUtensorMap* map, const void* base, long long BH, long long S, int d, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const CUtensorMapSwizzle sw = d == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                          : CU_TENSOR_MAP_SWIZZLE_NONE;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(BH)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(S) * d};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // 2-D map over the fp32 dQ accumulator [rows, d]: box = (32 columns, 128 rows),
 // 128-byte swizzle (the layout the backward kernel stages its dQ tile in).
 bool make_dq_map(CUtensorMap* map, const float* base, long long rows, int d) {
@@ -845,6 +863,248 @@ int attn_out_projection_bwd(const void* o, const void* w_o, const void* dy, void
   q.wd = p.wd;
   if (attn::launch_proj_bwd(to64, to64, to64, tdy64, tdy64, tdy64, tdo, q, s) != cudaSuccess) return ATTN_ERR_CUDA;
   return attn::launch_proj_reduce(ws, dw_o, hd * d_model, z, s) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- norm + rotation, caches, trees
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks shared by the norm + rotation calls; *empty is set when there is no row.
+static int check_norm_rope(int B, int h, int h_kv, int n, int d, int rot, int axes, const int* sections, float eps,
+                           const int* positions, const float* freqs, bool* empty) {
+  *empty = false;
+  if (B < 0 || h < 0 || h_kv < 0 || n < 0) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || !(eps > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (rot < 0 || rot > d) return ATTN_ERR_INVALID_ARG;
+  if (rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (axes < 1 || axes > 3) return ATTN_ERR_UNSUPPORTED;
+  if (sections != nullptr) {
+    long long sum = 0;
+    for (int i = 0; i < axes; ++i) {
+      if (sections[i] < 0) return ATTN_ERR_INVALID_ARG;
+      sum += sections[i];
+    }
+    if (sum != rot / 2) return ATTN_ERR_INVALID_ARG;
+  } else if (axes > 1) {
+    return ATTN_ERR_INVALID_ARG;
+  }
+  if (static_cast<long long>(h) + h_kv > 65535) return ATTN_ERR_UNSUPPORTED;  // grid y
+  if (static_cast<long long>(B) * n > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || n == 0 || (h == 0 && h_kv == 0)) {
+    *empty = true;
+    return ATTN_OK;
+  }
+  if (rot > 0 && (!positions || !freqs)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(positions) || !aligned4(freqs)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+static void fill_norm_rope(attn::NormRopeParams* p, const void* q, const void* k, const void* w_q, const void* w_k,
+                           const int* positions, const float* freqs, int B, int h, int h_kv, int n, int rot, int axes,
+                           const int* sections, int interleaved, float eps) {
+  p->q = static_cast<const __nv_bfloat16*>(q);
+  p->k = static_cast<const __nv_bfloat16*>(k);
+  p->w_q = static_cast<const __nv_bfloat16*>(w_q);
+  p->w_k = static_cast<const __nv_bfloat16*>(w_k);
+  p->pos = positions;
+  p->freq = freqs;
+  p->tokens = static_cast<long long>(B) * n;
+  p->n = n;
+  p->h = h;
+  p->h_kv = h_kv;
+  p->rot = rot;
+  p->axes = axes;
+  p->sec0 = axes > 1 ? sections[0] : rot;
+  p->sec1 = axes > 2 ? sections[0] + sections[1] : rot;
+  p->interleaved = interleaved ? 1 : 0;
+  p->eps = eps;
+}
+
+int attn_qk_norm_rope(const void* q, const void* k, const void* w_q, const void* w_k, const int* positions,
+                      const float* freqs, void* q_out, void* k_out, int B, int h, int h_kv, int n, int d, int rot,
+                      int axes, const int* sections, int interleaved, float eps, attn_stream_t stream) {
+  bool empty = false;
+  const int st = check_norm_rope(B, h, h_kv, n, d, rot, axes, sections, eps, positions, freqs, &empty);
+  if (st != ATTN_OK || empty) return st;
+  if (h > 0 && (!q || !w_q || !q_out || !aligned16(q) || !aligned16(w_q) || !aligned16(q_out)))
+    return ATTN_ERR_INVALID_ARG;
+  if (h_kv > 0 && (!k || !w_k || !k_out || !aligned16(k) || !aligned16(w_k) || !aligned16(k_out)))
+    return ATTN_ERR_INVALID_ARG;
+  attn::NormRopeParams p{};
+  fill_norm_rope(&p, q, k, w_q, w_k, positions, freqs, B, h, h_kv, n, rot, axes, sections, interleaved, eps);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  return attn::launch_norm_rope(d, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int B, int h, int h_kv, int n, int d) {
+  if (B <= 0 || h < 0 || h_kv < 0 || n <= 0 || (d != 32 && d != 64 && d != 128)) return 0;
+  const long long heads = static_cast<long long>(h) + h_kv;
+  if (heads < 1 || heads > 65535) return 0;
+  int gx = 0, gy = 0, per = 0;
+  attn::norm_rope_bwd_grid(d, static_cast<long long>(B) * n, static_cast<int>(heads), &gx, &gy, &per);
+  return static_cast<size_t>(gx) * gy * 2 * d * sizeof(float);
+}
+
+int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* w_q, const void* w_k, const int* positions,
+                          const float* freqs, const void* dq_out, const void* dk_out, void* dq, void* dk, void* dw_q,
+                          void* dw_k, int B, int h, int h_kv, int n, int d, int rot, int axes, const int* sections,
+                          int interleaved, float eps, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  bool empty = false;
+  const int st = check_norm_rope(B, h, h_kv, n, d, rot, axes, sections, eps, positions, freqs, &empty);
+  if (st != ATTN_OK) return st;
+  if (h > 0 && (!w_q || !dw_q || !aligned16(w_q) || !aligned16(dw_q))) return ATTN_ERR_INVALID_ARG;
+  if (h_kv > 0 && (!w_k || !dw_k || !aligned16(w_k) || !aligned16(dw_k))) return ATTN_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (empty) {  // no row: the weight gradients are zero
+    if (h > 0 && cudaMemsetAsync(dw_q, 0, static_cast<size_t>(d) * 2, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (h_kv > 0 && cudaMemsetAsync(dw_k, 0, static_cast<size_t>(d) * 2, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    return ATTN_OK;
+  }
+  if (h > 0 && (!q || !dq_out || !dq || !aligned16(q) || !aligned16(dq_out) || !aligned16(dq)))
+    return ATTN_ERR_INVALID_ARG;
+  if (h_kv > 0 && (!k || !dk_out || !dk || !aligned16(k) || !aligned16(dk_out) || !aligned16(dk)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(B, h, h_kv, n, d))
+    return ATTN_ERR_INVALID_ARG;
+  attn::NormRopeParams p{};
+  fill_norm_rope(&p, q, k, w_q, w_k, positions, freqs, B, h, h_kv, n, rot, axes, sections, interleaved, eps);
+  p.dq_out = static_cast<const __nv_bfloat16*>(dq_out);
+  p.dk_out = static_cast<const __nv_bfloat16*>(dk_out);
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dw_q = h > 0 ? static_cast<__nv_bfloat16*>(dw_q) : nullptr;
+  p.dw_k = h_kv > 0 ? static_cast<__nv_bfloat16*>(dw_k) : nullptr;
+  p.part = static_cast<float*>(workspace);
+  return attn::launch_norm_rope_bwd(d, p, s) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Checks shared by the cache calls (rows: the rows the grid covers).
+static int check_cache(int B, int h_kv, int m, int d, long long rows, const int* kv_len) {
+  if (B < 0 || h_kv < 0 || m < 1) return ATTN_ERR_INVALID_ARG;
+  if (d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * h_kv > 0x7fffffffLL || rows > (1ll << 34)) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(kv_len)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+int attn_cache_write(const void* k, const void* v, void* k_cache, void* v_cache, void* k_exp, void* v_exp,
+                     const int* kv_len, const int* new_len, int B, int h_kv, int n, int m, int d,
+                     attn_stream_t stream) {
+  if (n < 0) return ATTN_ERR_INVALID_ARG;
+  const long long BH = static_cast<long long>(B) * h_kv;
+  if (n > 0 && BH > (1ll << 34) / n) return ATTN_ERR_UNSUPPORTED;
+  const int st = check_cache(B, h_kv, m, d, BH * n, kv_len);
+  if (st != ATTN_OK) return st;
+  if (!aligned4(new_len)) return ATTN_ERR_INVALID_ARG;
+  if (BH == 0 || n == 0) return ATTN_OK;
+  if (!k || !v || !k_cache || !v_cache || (k_exp == nullptr) != (v_exp == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache)) return ATTN_ERR_INVALID_ARG;
+  attn::CacheParams p{};
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_exp = static_cast<unsigned char*>(k_exp);
+  p.v_exp = static_cast<unsigned char*>(v_exp);
+  p.kv_len = kv_len;
+  p.new_len = new_len;
+  p.rows = BH * n;
+  p.h_kv = h_kv;
+  p.n = n;
+  p.m = m;
+  return attn::launch_cache_write(d, k_exp != nullptr, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_exp, const void* v_exp, void* k, void* v,
+                    const int* kv_len, int B, int h_kv, int m, int d, attn_stream_t stream) {
+  const long long BH = static_cast<long long>(B) * h_kv;
+  if (m > 0 && BH > (1ll << 34) / m) return ATTN_ERR_UNSUPPORTED;
+  const int st = check_cache(B, h_kv, m, d, BH * m, kv_len);
+  if (st != ATTN_OK) return st;
+  if (BH == 0) return ATTN_OK;
+  if (!k_cache || !v_cache || !k_exp || !v_exp || !k || !v) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache)) return ATTN_ERR_INVALID_ARG;
+  attn::CacheParams p{};
+  p.k_cache = const_cast<void*>(k_cache);
+  p.v_cache = const_cast<void*>(v_cache);
+  p.k_exp = static_cast<unsigned char*>(const_cast<void*>(k_exp));
+  p.v_exp = static_cast<unsigned char*>(const_cast<void*>(v_exp));
+  p.k_out = static_cast<__nv_bfloat16*>(k);
+  p.v_out = static_cast<__nv_bfloat16*>(v);
+  p.kv_len = kv_len;
+  p.rows = BH * m;
+  p.h_kv = h_kv;
+  p.m = m;
+  return attn::launch_cache_read(d, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK
+                                                                                              : ATTN_ERR_CUDA;
+}
+
+// Sizes of a tree step (B, h, h_kv >= 1 where there is work): ATTN_OK or the status to return.
+static int check_tree(int B, int h, int h_kv, int n, int m, int d) {
+  if (B < 0 || h < 0 || h_kv < 0 || m < 1 || n < 1 || n > attn::kTreeMaxN) return ATTN_ERR_INVALID_ARG;
+  if (d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (h_kv == 0 ? h != 0 : h % h_kv != 0) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * h_kv > 65535 || static_cast<long long>(h) * n > 0xfffffLL)
+    return ATTN_ERR_UNSUPPORTED;  // grid y, z
+  return ATTN_OK;
+}
+
+size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int m, int d) {
+  if (check_tree(B, h, h_kv, n, m, d) != ATTN_OK || B == 0 || h == 0) return 0;
+  const long long BH = static_cast<long long>(B) * h_kv;
+  const int rows = h / h_kv * n;
+  // enough for either cache type
+  const int a = attn::tree_splits(BH, rows, m, d, false), b = attn::tree_splits(BH, rows, m, d, true);
+  const int splits = a > b ? a : b;
+  return splits == 1 ? 0 : static_cast<size_t>(BH) * splits * rows * (static_cast<size_t>(d) + 2) * sizeof(float);
+}
+
+int attn_decode_tree(const void* q, const void* k, const void* v, void* o, float* lse, const void* k_exp,
+                     const void* v_exp, const int* kv_len, const long long* tree, int B, int h, int h_kv, int n, int m,
+                     int d, float scale, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  const int st = check_tree(B, h, h_kv, n, m, d);
+  if (st != ATTN_OK) return st;
+  if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || h == 0) return ATTN_OK;
+  if (!q || !k || !v || !o || (k_exp == nullptr) != (v_exp == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(lse) || !aligned4(kv_len) || (reinterpret_cast<uintptr_t>(tree) & 7u) != 0)
+    return ATTN_ERR_INVALID_ARG;
+  const size_t need = attn_decode_tree_workspace_bytes(B, h, h_kv, n, m, d);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+  const long long BH = static_cast<long long>(B) * h_kv;
+  const bool quantised = k_exp != nullptr;
+  const int tile = attn::tree_tile(d, quantised);
+  CUtensorMap tk, tv;
+  if (quantised ? (!make_code_map(&tk, k, BH, m, d, tile) || !make_code_map(&tv, v, BH, m, d, tile))
+                : (!make_tile_map(&tk, k, BH, m, d, tile) || !make_tile_map(&tv, v, BH, m, d, tile)))
+    return ATTN_ERR_CUDA;
+  uint32_t* status = nullptr;
+  if (device_status_word(&status) != cudaSuccess) return ATTN_ERR_CUDA;
+  attn::TreeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.part = static_cast<float*>(workspace);
+  p.tree = reinterpret_cast<const unsigned long long*>(tree);
+  p.kv_len = kv_len;
+  p.k_exp = static_cast<const unsigned char*>(k_exp);
+  p.v_exp = static_cast<const unsigned char*>(v_exp);
+  p.h_kv = h_kv;
+  p.n = n;
+  p.rows = h / h_kv * n;
+  p.m = m;
+  p.splits = attn::tree_splits(BH, p.rows, m, d, quantised);
+  p.c = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  p.wd.status = status;
+  p.wd.budget_ns = g_watchdog_ns.load();
+  const cudaError_t e = attn::launch_tree(d, quantised, tk, tv, p, static_cast<int>(BH),
+                                          reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 int attn_get_device_status(attn_stream_t stream) {

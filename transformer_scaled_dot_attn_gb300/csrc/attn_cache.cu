@@ -1,0 +1,202 @@
+// Writing new keys and values into a decoding cache, quantised as they are
+// written, and reading a quantised cache back.
+//
+// A quantised row (one position of one head) is d e4m3 codes and one exponent
+// byte: e is the least integer with max|x| <= 448 2^e (448 is e4m3's largest
+// value), kept in [-117, 119], and 0 for a row of zeros; code = x 2^-e rounded
+// to e4m3 (nearest even, saturating); byte = e + 127. A power of two as the
+// scale costs a floating-point code no precision (every code keeps its four
+// significant bits; at most one of e4m3's fifteen binades is given away) and
+// makes both directions exact but for the one rounding to e4m3: the division is
+// exact, and code 2^e is a bf16 number, so reading back rounds nothing.
+//
+// Both kernels stream each byte once (HBM bound). A thread owns 16 columns of
+// a row of K and the same of V: two 32-byte reads and two 16-byte writes (or
+// the reverse) in flight, and log2(d / 16) shuffles for the row maximum.
+#include "attn_kernels.cuh"
+
+namespace attn {
+namespace {
+
+using namespace sm103;
+
+constexpr int kCacheThreads = 256;
+
+struct Row16 {
+  uint4 a, b;  // 16 bf16
+};
+
+// Largest finite |x| of the 16 values, as bf16 bits (0 when there is none).
+__device__ __forceinline__ uint32_t finite_max(const Row16& r) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+    m = max(m, lo < 0x7f80u ? lo : 0u);
+    m = max(m, hi < 0x7f80u ? hi : 0u);
+  }
+  return m;
+}
+
+// The scale exponent of a row whose largest finite magnitude has these bf16
+// bits: 448 = 1.75 2^8, so e = exponent - 8, one more where the significand
+// is above 1.75 (its 7 stored bits above 0x60).
+__device__ __forceinline__ int scale_exponent(uint32_t amax) {
+  if (amax == 0) return 0;
+  const int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7fu) > 0x60u ? 1 : 0);
+  return min(max(e, -117), 119);
+}
+
+__device__ __forceinline__ uint32_t quantise4(uint32_t lo, uint32_t hi, float inv) {
+  const float2 x = unpack_bf16x2(lo), y = unpack_bf16x2(hi);
+  uint16_t a, b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x.y * inv), "f"(x.x * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(y.y * inv), "f"(y.x * inv));
+  return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
+}
+
+template <int D>
+__device__ __forceinline__ void write_row(const Row16& r, unsigned char* cache, unsigned char* exps, size_t row,
+                                          int tau, bool live) {
+  constexpr int T = D / 16;
+  uint32_t m = finite_max(r);
+#pragma unroll
+  for (int o = T / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int e = scale_exponent(m);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, a normal number
+  if (!live) return;
+  uint4 c;
+  c.x = quantise4(r.a.x, r.a.y, inv);
+  c.y = quantise4(r.a.z, r.a.w, inv);
+  c.z = quantise4(r.b.x, r.b.y, inv);
+  c.w = quantise4(r.b.z, r.b.w, inv);
+  *reinterpret_cast<uint4*>(cache + row * D + tau * 16) = c;
+  if (tau == 0) exps[row] = static_cast<unsigned char>(e + 127);
+}
+
+// New row i of sequence b goes to position L_b - new_b + i; rows past new_b and
+// positions outside the cache are left alone.
+template <int D, bool QUANT>
+__global__ void __launch_bounds__(kCacheThreads) attn_cache_write_kernel(const CacheParams p) {
+  constexpr int T = D / 16;
+  const int tau = threadIdx.x % T;
+  const long long row = static_cast<long long>(blockIdx.x) * (kCacheThreads / T) + threadIdx.x / T;
+  bool live = row < p.rows;
+  const long long bg = live ? row / p.n : 0;
+  const int i = live ? static_cast<int>(row - bg * p.n) : 0;
+  const int b = static_cast<int>(bg / p.h_kv);
+  const int L = p.kv_len == nullptr ? p.m : min(max(__ldg(p.kv_len + b), 0), p.m);
+  const int nn = p.new_len == nullptr ? p.n : min(max(__ldg(p.new_len + b), 0), p.n);
+  const int at = L - nn + i;
+  live = live && i < nn && at >= 0;  // at < L <= m since i < nn
+  Row16 k = {}, v = {};
+  if (live) {
+    const size_t src = static_cast<size_t>(row) * D + tau * 16;
+    k.a = *reinterpret_cast<const uint4*>(p.k + src);
+    k.b = *reinterpret_cast<const uint4*>(p.k + src + 8);
+    v.a = *reinterpret_cast<const uint4*>(p.v + src);
+    v.b = *reinterpret_cast<const uint4*>(p.v + src + 8);
+  }
+  const size_t dst = static_cast<size_t>(bg) * p.m + (live ? at : 0);
+  if constexpr (QUANT) {
+    write_row<D>(k, static_cast<unsigned char*>(p.k_cache), p.k_exp, dst, tau, live);
+    write_row<D>(v, static_cast<unsigned char*>(p.v_cache), p.v_exp, dst, tau, live);
+  } else if (live) {
+    __nv_bfloat16* kc = static_cast<__nv_bfloat16*>(p.k_cache) + dst * D + tau * 16;
+    __nv_bfloat16* vc = static_cast<__nv_bfloat16*>(p.v_cache) + dst * D + tau * 16;
+    *reinterpret_cast<uint4*>(kc) = k.a;
+    *reinterpret_cast<uint4*>(kc + 8) = k.b;
+    *reinterpret_cast<uint4*>(vc) = v.a;
+    *reinterpret_cast<uint4*>(vc + 8) = v.b;
+  }
+}
+
+// Two codes times 2^e as a bf16 pair (exact: see above).
+__device__ __forceinline__ uint32_t dequantise2(uint32_t two, float scale) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(two)));
+  float lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h2));
+  return pack_bf16x2(lo * scale, hi * scale);
+}
+
+__device__ __forceinline__ void read_row(const unsigned char* cache, const unsigned char* exps, __nv_bfloat16* out,
+                                         size_t row, size_t at, bool real) {
+  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+  if (real) {
+    const uint4 c = __ldg(reinterpret_cast<const uint4*>(cache + at));
+    const int byte = __ldg(exps + row);
+    // 2^(byte - 127); byte 0 is 2^-127, a subnormal number; 255 (never written) reads as infinity
+    const float s = byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(byte) << 23);
+    lo = make_uint4(dequantise2(c.x & 0xffffu, s), dequantise2(c.x >> 16, s), dequantise2(c.y & 0xffffu, s),
+                    dequantise2(c.y >> 16, s));
+    hi = make_uint4(dequantise2(c.z & 0xffffu, s), dequantise2(c.z >> 16, s), dequantise2(c.w & 0xffffu, s),
+                    dequantise2(c.w >> 16, s));
+  }
+  *reinterpret_cast<uint4*>(out + at) = lo;
+  *reinterpret_cast<uint4*>(out + at + 8) = hi;
+}
+
+// Rows at or past the sequence's length come back as zeros (their cache bytes are not read).
+template <int D>
+__global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const CacheParams p) {
+  constexpr int T = D / 16;
+  const int tau = threadIdx.x % T;
+  const long long row = static_cast<long long>(blockIdx.x) * (kCacheThreads / T) + threadIdx.x / T;
+  if (row >= p.rows) return;
+  const long long bg = row / p.m;
+  const int j = static_cast<int>(row - bg * p.m);
+  const int b = static_cast<int>(bg / p.h_kv);
+  const int L = p.kv_len == nullptr ? p.m : __ldg(p.kv_len + b);
+  const size_t at = static_cast<size_t>(row) * D + tau * 16;
+  const bool real = j < L;
+  read_row(static_cast<const unsigned char*>(p.k_cache), p.k_exp, p.k_out, row, at, real);
+  read_row(static_cast<const unsigned char*>(p.v_cache), p.v_exp, p.v_out, row, at, real);
+}
+
+template <int D>
+cudaError_t launch_write_d(bool quantised, const CacheParams& p, cudaStream_t stream) {
+  constexpr int RB = kCacheThreads / (D / 16);
+  const unsigned blocks = static_cast<unsigned>((p.rows + RB - 1) / RB);
+  prof_begin(kKindCache, stream);
+  if (quantised) attn_cache_write_kernel<D, true><<<blocks, kCacheThreads, 0, stream>>>(p);
+  else attn_cache_write_kernel<D, false><<<blocks, kCacheThreads, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  prof_end(kKindCache, stream);
+  return e;
+}
+
+template <int D>
+cudaError_t launch_read_d(const CacheParams& p, cudaStream_t stream) {
+  constexpr int RB = kCacheThreads / (D / 16);
+  prof_begin(kKindCache, stream);
+  attn_cache_read_kernel<D><<<static_cast<unsigned>((p.rows + RB - 1) / RB), kCacheThreads, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  prof_end(kKindCache, stream);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(int d, bool quantised, const CacheParams& p, cudaStream_t stream) {
+  switch (d) {
+    case 32: return launch_write_d<32>(quantised, p, stream);
+    case 64: return launch_write_d<64>(quantised, p, stream);
+    case 128: return launch_write_d<128>(quantised, p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_cache_read(int d, const CacheParams& p, cudaStream_t stream) {
+  switch (d) {
+    case 32: return launch_read_d<32>(p, stream);
+    case 64: return launch_read_d<64>(p, stream);
+    case 128: return launch_read_d<128>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace attn

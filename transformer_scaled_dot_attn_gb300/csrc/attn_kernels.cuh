@@ -19,7 +19,8 @@ constexpr uint32_t kDevLayout = 0x200u;
 enum WaitSite : uint32_t {
   kSiteQFull = 1, kSiteKFull, kSiteVFull, kSiteKEmpty, kSiteVEmpty, kSiteSFull,
   kSitePFull, kSiteOFull, kSiteDrain, kSiteBwdLoad, kSiteBwdS, kSiteBwdDP, kSiteBwdDS,
-  kSiteBwdDQ, kSiteBwdFree, kSiteBwdFinal, kSiteExpTurn
+  kSiteBwdDQ, kSiteBwdFree, kSiteBwdFinal, kSiteExpTurn,
+  kSiteTree
 };
 
 struct Watchdog {
@@ -84,7 +85,7 @@ __device__ __forceinline__ void query_range(int k0, int k1, int n, int causal, i
 // with CUDA events on `stream` when profiling is enabled; no-ops otherwise.
 enum KernelKind : int {
   kKindFwd = 0, kKindBwdPre = 1, kKindBwdMain = 2, kKindBwdPost = 3, kKindDecode = 4, kKindDecodeMerge = 5,
-  kKindProj = 6, kNumKinds = 7
+  kKindProj = 6, kKindNormRope = 7, kKindCache = 8, kKindTree = 9, kKindTreeMerge = 10, kNumKinds = 11
 };
 void prof_begin(int kind, cudaStream_t stream);
 void prof_end(int kind, cudaStream_t stream);
@@ -251,5 +252,68 @@ cudaError_t launch_proj_bwd(const CUtensorMap& ta0, const CUtensorMap& ta1, cons
 int proj_bwd_splits(int M, int N, int chunks);
 // out (bf16) = sum over splits of part[z][0 .. count), count a multiple of 8.
 cudaError_t launch_proj_reduce(const float* part, void* out, long long count, int splits, cudaStream_t stream);
+
+// ---------------------------------------------------------------- norm + rotation
+
+constexpr int kSms = 152;  // SMs of the GPU this library is built for (grid sizes only)
+
+struct NormRopeParams {
+  const __nv_bfloat16 *q, *k;          // [B, h, n, d], [B, h_kv, n, d]
+  const __nv_bfloat16 *w_q, *w_k;      // [d]
+  const int* pos;                      // [axes, B, n]
+  const float* freq;                   // [rot / 2]
+  __nv_bfloat16 *q_out, *k_out;        // forward results
+  const __nv_bfloat16 *dq_out, *dk_out;  // backward: upstream gradients
+  __nv_bfloat16 *dq, *dk;              // backward: input gradients
+  __nv_bfloat16 *dw_q, *dw_k;          // backward: weight gradients [d]
+  float* part;                         // backward: fp32 partials [blocks][2][d]
+  long long tokens;                    // B n
+  long long token_blocks;              // set by the launcher
+  int n, h, h_kv, rot, axes;
+  int sec0, sec1;                      // pairs from sec0 (sec1) on turn by axis 1 (2)
+  int interleaved;
+  int heads_per;                       // heads a block loops over; set by the launcher
+  float eps;
+};
+void norm_rope_bwd_grid(int d, long long tokens, int heads, int* gx, int* gy, int* heads_per);
+cudaError_t launch_norm_rope(int d, const NormRopeParams& p, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(int d, const NormRopeParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- cache
+
+struct CacheParams {
+  const __nv_bfloat16 *k, *v;      // write: new rows [B, h_kv, n, d]
+  void *k_cache, *v_cache;         // [B, h_kv, m, d], bf16 or e4m3
+  unsigned char *k_exp, *v_exp;    // [B, h_kv, m] scale exponents + 127 (e4m3)
+  __nv_bfloat16 *k_out, *v_out;    // read: [B, h_kv, m, d]
+  const int* kv_len;               // [B] or nullptr (m)
+  const int* new_len;              // [B] or nullptr (n)
+  long long rows;                  // write: B h_kv n; read: B h_kv m
+  int h_kv, n, m;
+};
+cudaError_t launch_cache_write(int d, bool quantised, const CacheParams& p, cudaStream_t stream);
+cudaError_t launch_cache_read(int d, const CacheParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- tree decoding
+
+constexpr int kTreeMaxN = 64;       // drafted tokens per step (bits of a mask word)
+
+struct TreeParams {
+  const __nv_bfloat16* q;          // [B h_kv][rows][d]: the query heads of a key head are neighbours
+  __nv_bfloat16* o;                // like q
+  float* lse;                      // [B h_kv][rows] or nullptr
+  float* part;                     // [B h_kv][splits][rows][d + 2] fp32 partials
+  const unsigned long long* tree;  // [B][n] or nullptr (causal)
+  const int* kv_len;               // [B] or nullptr
+  const unsigned char *k_exp, *v_exp;  // [B h_kv][m] (e4m3 caches)
+  int h_kv, n, rows, m, splits;    // rows = (h / h_kv) n
+  float c;                         // scale log2(e)
+  Watchdog wd;
+};
+// Rows the key tiles' TMA box holds, for the cache type and head size.
+int tree_tile(int d, bool quantised);
+int tree_splits(long long BH, int rows, int m, int d, bool quantised);
+cudaError_t launch_tree(int d, bool quantised, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                        int BH, cudaStream_t stream);
 
 }  // namespace attn

@@ -1,0 +1,681 @@
+// Decoding of drafted tokens over a cache: the n newest positions of each
+// sequence (n <= 64) are queries, hanging on one another as a tree. Every query
+// sees all positions before the newest n and, of the newest n, those whose bit
+// is set in its mask word (its ancestors and itself; without masks: the
+// positions up to its own). h / h_kv query heads share a key head, and their
+// queries of one sequence are neighbours in memory, so a key head faces one
+// matrix of rows = (h / h_kv) n queries:
+//
+//   x_rj = scale q_r . k_j over the visible j,  O_r = sum_j softmax(x_r)_j v_j,  lse_r = ln sum_j exp(x_rj).
+//
+// The caches are bf16, or e4m3 codes with a power-of-two scale a row.
+//
+// With few rows a step is bound by reading the cache once. The keys of a head
+// are split over CTAs by the sequence's own length (every CTA of a sequence
+// gets the same number of tiles, whatever the capacity), and over the four warps
+// of a CTA: each warp streams its own tiles through its own TMA ring and keeps
+// its own running maximum, so the loop has no CTA barrier. The products run on
+// mma.sync with 16 query rows (a tcgen05 tile has 128 rows, most of them idle
+// here, and its operands would have to be written out in 16 bits first). The
+// warps' results are joined in shared memory, the CTAs' by a second kernel.
+#include "attn_kernels.cuh"
+
+#include <atomic>
+
+namespace attn {
+namespace {
+
+using namespace sm103;
+
+constexpr int kTreeWarps = 4;
+constexpr int kTreeThreads = kTreeWarps * 32;
+constexpr int kTreeRows = 16;  // query rows of a CTA (one mma.sync tile)
+constexpr float kTreeLn2 = 0.69314718055994530942f;
+
+template <int D, bool Q8>
+struct Tree {
+  static constexpr int ES = Q8 ? 1 : 2;                    // bytes of a cache element
+  static constexpr int TK = (D == 128 && !Q8) ? 16 : 32;   // keys per tile of a warp
+  static constexpr uint32_t KT = TK * D * ES;              // one K (or V) tile
+  static constexpr uint32_t ROWB = D * ES <= 128 ? D * ES : 128;  // bytes of a row in a TMA box
+  static constexpr uint32_t BOX = TK * ROWB;
+  static constexpr int NBOX = D * ES / ROWB;
+  static constexpr int STAGES = 3;
+  static constexpr int NT = TK / 8;                        // n8 score tiles
+  static constexpr int KS = D / 16;                        // k steps of the score product
+  static constexpr uint32_t RING = kTreeWarps * STAGES * 2 * KT;
+  static constexpr int OST = D + 4;                        // row pitch of the join area (fp32)
+  static constexpr uint32_t JOIN = kTreeWarps * kTreeRows * OST * 4;
+  static constexpr uint32_t SMEM = (RING > JOIN ? RING : JOIN) + 1024;  // + alignment slack
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Two e4m3 codes (the halves' high bytes) as a bf16 pair: the code's exponent
+// and significand moved to bf16's places stand for its value times 2^-120
+// (bias 7 against 127; subnormal codes included), which one exact product
+// undoes. The NaN code comes out as 480 here; nan_codes finds it.
+__device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t high_bytes) {
+  const uint32_t x = ((high_bytes >> 4) & 0x07f007f0u) | (high_bytes & 0x80008000u);
+  const uint32_t up = 0x7b807b80u;  // 2^120, twice
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(up));
+  return r;
+}
+
+// Bit 7 of a byte of the result is set where that code is NaN (0x7f, 0xff).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// e4m3 caches: which key of a group of eight stands in column g of a product.
+// The order is chosen so that the threads that read shared memory together
+// meet every bank once, for K (rows of neighbouring g) and V (rows of one t).
+template <int D>
+__device__ __forceinline__ int key_of(int g) {
+  const int t = g >> 1;
+  if (D == 128) return t + 4 * (g & 1);
+  if (D == 64) return ((t & 1) + 4 * (t >> 1)) ^ ((g & 1) * 3);
+  return (g & 1) ? (t ^ 2) + 4 : t;
+}
+
+// e4m3 caches, d = 128: the 16-byte column chunk of product column g (same reason).
+template <int D>
+__device__ __forceinline__ int col_of(int g) {
+  return D == 128 ? (g >> 1) + 4 * (g & 1) : g;
+}
+
+// Byte offset of byte `at` of row r in a tile as TMA's swizzle lays it out.
+template <int D, bool Q8>
+__device__ __forceinline__ uint32_t tile_off(int r, int at) {
+  using C = Tree<D, Q8>;
+  const int box = at / static_cast<int>(C::ROWB), in = at % static_cast<int>(C::ROWB);
+  const int chunk = in >> 4, low = in & 15;
+  const int pc = C::ROWB == 128 ? (chunk ^ (r & 7)) : C::ROWB == 64 ? (chunk ^ ((r >> 1) & 3)) : chunk;
+  return box * C::BOX + r * C::ROWB + (pc << 4) + low;
+}
+
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          const Watchdog& wd) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > wd.budget_ns) {
+      *abort_flag = 1;
+      atomicCAS(wd.status, 0u, kDevTimeout | kSiteTree);
+      return false;
+    }
+  }
+  return true;
+}
+
+// Copies in flight must land before the CTA's shared memory goes away.
+__device__ __forceinline__ void tree_drain(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > wd.budget_ns) {
+      atomicCAS(wd.status, 0u, kDevTimeout | kSiteDrain);
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ float pow2_of_byte(int byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : static_cast<uint32_t>(byte) << 23);
+}
+
+// Key tiles a split of a sequence with L cached positions takes.
+__device__ __forceinline__ int tiles_per_split(int L, int tk, int splits) {
+  return ((L + tk - 1) / tk + splits - 1) / splits;
+}
+
+// The newest positions a query sees: bit t stands for position L - n + t.
+__device__ __forceinline__ unsigned long long tree_word(const TreeParams& p, int b, int row) {
+  const int i = row % p.n;
+  if (p.tree != nullptr) return __ldg(p.tree + static_cast<size_t>(b) * p.n + i);
+  return i >= 63 ? ~0ull : (1ull << (i + 1)) - 1ull;
+}
+
+__device__ __forceinline__ bool sees(unsigned long long word, int key, int old, int L) {
+  return key < L && (key < old || ((word >> (key - old)) & 1ull));
+}
+
+template <int D, bool Q8>
+__device__ __forceinline__ float value_at(const uint8_t* tile, int r, int c) {
+  if constexpr (Q8) {
+    const uint32_t code = tile[tile_off<D, true>(r, c)];
+    if ((code & 0x7fu) == 0x7fu) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(e4m3_to_bf16x2(code << 8) << 16);
+  } else {
+    const uint16_t h = *reinterpret_cast<const uint16_t*>(tile + tile_off<D, false>(r, 2 * c));
+    return __uint_as_float(static_cast<uint32_t>(h) << 16);
+  }
+}
+
+// Zeroes the halves of a value pair that may not enter a product: keys at or
+// past L (what the cache holds there is anyone's) and values that are not
+// finite (a weight of 0 would make them NaN for rows that do not see them;
+// `odd` reports them, and the rows that do see them add them afterwards).
+__device__ __forceinline__ uint32_t clean_pair(uint32_t v, bool lo_real, bool hi_real, bool& odd) {
+  if (!lo_real) v &= 0xffff0000u;
+  if (!hi_real) v &= 0x0000ffffu;
+  if ((v & 0x7f80u) == 0x7f80u) {
+    odd = true;
+    v &= 0xffff0000u;
+  }
+  if ((v & 0x7f800000u) == 0x7f800000u) {
+    odd = true;
+    v &= 0x0000ffffu;
+  }
+  return v;
+}
+
+// Grid: x = key split, y = (sequence, key head), z = block of 16 query rows.
+template <int D, bool Q8>
+__global__ void __launch_bounds__(kTreeThreads)
+attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const TreeParams p) {
+  using C = Tree<D, Q8>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kTreeWarps][C::STAGES];
+  __shared__ int abort_word;
+  __shared__ float s_m[kTreeWarps][kTreeRows], s_l[kTreeWarps][kTreeRows];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int split = blockIdx.x, bh = blockIdx.y, row0 = blockIdx.z * kTreeRows;
+  const int b = bh / p.h_kv;
+  const int L = head_keys(p.kv_len, bh, p.h_kv, p.m);
+  const int old = L - p.n;  // positions before the newest n (negative: fewer cached than n)
+  const int per = tiles_per_split(L, C::TK, p.splits);
+  const int tile0 = split * per, tile1 = min((L + C::TK - 1) / C::TK, tile0 + per);
+  if (tile0 >= tile1 && split > 0) return;  // split 0 also stands for an empty cache
+  volatile int* abort_flag = &abort_word;
+  const Watchdog wd = p.wd;
+  if (tid == 0) {
+    for (int w = 0; w < kTreeWarps; ++w)
+      for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[w][s], 1);
+    abort_word = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  __syncthreads();
+
+  // this warp's tiles: tile0 + warp, then every fourth
+  const int mine = tile1 - tile0 > warp ? (tile1 - tile0 - warp + kTreeWarps - 1) / kTreeWarps : 0;
+  uint8_t* ring = smem + warp * (C::STAGES * 2 * C::KT);
+  auto load = [&](int x) {
+    const int st = x % C::STAGES;
+    const int k0 = (tile0 + warp + x * kTreeWarps) * C::TK;
+    uint8_t* dst = ring + st * 2 * C::KT;
+    mbar_arrive_expect_tx(&full[warp][st], 2 * C::KT);
+    for (int a = 0; a < C::NBOX; ++a) {
+      tma_load_3d(dst + a * C::BOX, &tm_k, &full[warp][st], a * (C::ROWB / C::ES), k0, bh);
+      tma_load_3d(dst + C::KT + a * C::BOX, &tm_v, &full[warp][st], a * (C::ROWB / C::ES), k0, bh);
+    }
+  };
+  if (lane == 0)
+    for (int x = 0; x < C::STAGES && x < mine; ++x) load(x);
+
+  // the queries as the A operand: rows g and g + 8 of the block. e4m3 caches
+  // multiply in f16, which holds every code; the query row is brought to
+  // [2^14, 2^15) by a power of two first, so that what f16 cannot hold of it
+  // lies 2^-39 below its largest element.
+  const int r0 = row0 + g, r1 = r0 + 8;
+  const __nv_bfloat16* qrow0 = p.q + (static_cast<size_t>(bh) * p.rows + min(r0, p.rows - 1)) * D;
+  const __nv_bfloat16* qrow1 = p.q + (static_cast<size_t>(bh) * p.rows + min(r1, p.rows - 1)) * D;
+  uint32_t qa[C::KS][4];
+  float c0 = p.c, c1 = p.c;  // per row: scale log2(e), and for e4m3 the inverse of the query's power of two
+  if constexpr (Q8) {
+    uint32_t a0 = 0, a1 = 0;
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s) {
+      const int at = D == 128 ? 16 * (t + 4 * (s >> 2)) + 4 * (s & 3) : D == 64 ? 16 * t + 4 * s : 8 * t + 4 * s;
+      const uint2 u = *reinterpret_cast<const uint2*>(qrow0 + at);
+      const uint2 v = *reinterpret_cast<const uint2*>(qrow1 + at);
+      qa[s][0] = u.x;
+      qa[s][1] = v.x;
+      qa[s][2] = u.y;
+      qa[s][3] = v.y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = qa[s][e] & 0x7fffu, hi = (qa[s][e] >> 16) & 0x7fffu;
+        uint32_t& a = (e & 1) ? a1 : a0;
+        a = max(a, lo < 0x7f80u ? lo : 0u);
+        a = max(a, hi < 0x7f80u ? hi : 0u);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+      a0 = max(a0, __shfl_xor_sync(0xffffffffu, a0, o));
+      a1 = max(a1, __shfl_xor_sync(0xffffffffu, a1, o));
+    }
+    const uint32_t e0 = 268u - max(a0 >> 7, 15u), e1 = 268u - max(a1 >> 7, 15u);
+    const float u0 = __uint_as_float(e0 << 23), u1 = __uint_as_float(e1 << 23);
+    c0 *= __uint_as_float((254u - e0) << 23);
+    c1 *= __uint_as_float((254u - e1) << 23);
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = unpack_bf16x2(qa[s][e]);
+        const float f = (e & 1) ? u1 : u0;
+        qa[s][e] = pack_f16x2(x.x * f, x.y * f);
+      }
+  } else {
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s) {
+      qa[s][0] = *reinterpret_cast<const uint32_t*>(qrow0 + 16 * s + 2 * t);
+      qa[s][1] = *reinterpret_cast<const uint32_t*>(qrow1 + 16 * s + 2 * t);
+      qa[s][2] = *reinterpret_cast<const uint32_t*>(qrow0 + 16 * s + 8 + 2 * t);
+      qa[s][3] = *reinterpret_cast<const uint32_t*>(qrow1 + 16 * s + 8 + 2 * t);
+    }
+  }
+  const unsigned long long word0 = tree_word(p, b, min(r0, p.rows - 1));
+  const unsigned long long word1 = tree_word(p, b, min(r1, p.rows - 1));
+  // keys of score columns 2t and 2t + 1 within a group of eight
+  const int ka = Q8 ? key_of<D>(2 * t) : 2 * t, kb = Q8 ? key_of<D>(2 * t + 1) : 2 * t + 1;
+
+  float acc[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this thread's columns only
+
+  // e4m3: lane j holds the scale bytes of key j of the tile, read one tile ahead
+  int ke = 127, ve = 127;
+  auto scales = [&](int x) {
+    const int key = (tile0 + warp + x * kTreeWarps) * C::TK + lane;
+    const bool in = x < mine && key < L;
+    const size_t at = static_cast<size_t>(bh) * p.m + key;
+    ke = in ? __ldg(p.k_exp + at) : 127;
+    ve = in ? __ldg(p.v_exp + at) : 127;
+  };
+  if constexpr (Q8) scales(0);
+
+  int x = 0;
+  for (; x < mine; ++x) {
+    const int st = x % C::STAGES;
+    const int k0 = (tile0 + warp + x * kTreeWarps) * C::TK;
+    const uint8_t* sk = ring + st * 2 * C::KT;
+    const uint8_t* sv = sk + C::KT;
+    const uint32_t ak = smem_u32(sk), av = smem_u32(sv);
+    const int my_ke = ke, my_ve = ve;
+    if constexpr (Q8) scales(x + 1);
+    if (!__all_sync(0xffffffffu, tree_wait(&full[warp][st], (x / C::STAGES) & 1, abort_flag, wd))) break;
+
+    // scores of the tile's keys
+    float s[C::NT][4];
+#pragma unroll
+    for (int i = 0; i < C::NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+    if constexpr (Q8) {
+#pragma unroll
+      for (int i = 0; i < C::NT; ++i) {
+        const int r = i * 8 + key_of<D>(g);
+        uint32_t w[D / 16];
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + tile_off<D, true>(r, 16 * t));
+          const uint4 v = *reinterpret_cast<const uint4*>(sk + tile_off<D, true>(r, 16 * (t + 4)));
+          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+          w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+        } else if constexpr (D == 64) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + tile_off<D, true>(r, 16 * t));
+          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(sk + tile_off<D, true>(r, 8 * t));
+          w[0] = u.x, w[1] = u.y;
+        }
+#pragma unroll
+        for (int k = 0; k < C::KS; ++k)
+          mma_f16(s[i], qa[k], e4m3_to_f16x2(w[k] & 0xffffu), e4m3_to_f16x2(w[k] >> 16));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < C::KS; k += 2)
+#pragma unroll
+        for (int i = 0; i < C::NT; ++i) {
+          uint32_t w[4];
+          ldsm4(ak + tile_off<D, false>(i * 8 + (lane & 7), (2 * k + (lane >> 3)) * 16), w);
+          mma_bf16(s[i], qa[k], w[0], w[1]);
+          mma_bf16(s[i], qa[k + 1], w[2], w[3]);
+        }
+    }
+    // in units of log2, masked where the tile reaches past the positions that every row sees
+    const bool tail = k0 + C::TK > old;
+    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < C::NT; ++i) {
+      float fa = 1.f, fb = 1.f;
+      if constexpr (Q8) {
+        fa = pow2_of_byte(__shfl_sync(0xffffffffu, my_ke, i * 8 + ka));
+        fb = pow2_of_byte(__shfl_sync(0xffffffffu, my_ke, i * 8 + kb));
+      }
+      s[i][0] *= c0 * fa;
+      s[i][1] *= c0 * fb;
+      s[i][2] *= c1 * fa;
+      s[i][3] *= c1 * fb;
+      if (tail) {
+        const int ja = k0 + i * 8 + ka, jb = k0 + i * 8 + kb;
+        if (!sees(word0, ja, old, L)) s[i][0] = -INFINITY;
+        if (!sees(word0, jb, old, L)) s[i][1] = -INFINITY;
+        if (!sees(word1, ja, old, L)) s[i][2] = -INFINITY;
+        if (!sees(word1, jb, old, L)) s[i][3] = -INFINITY;
+      }
+      t0 = fmaxf(t0, fmaxf(s[i][0], s[i][1]));
+      t1 = fmaxf(t1, fmaxf(s[i][2], s[i][3]));
+    }
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, o));
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, o));
+    }
+    if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
+      const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+      const float a0 = ex2_approx(m0 - (n0 == -INFINITY ? 0.f : n0)), a1 = ex2_approx(m1 - (n1 == -INFINITY ? 0.f : n1));
+      m0 = n0;
+      m1 = n1;
+      l0 *= a0;
+      l1 *= a1;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        acc[i][0] *= a0;
+        acc[i][1] *= a0;
+        acc[i][2] *= a1;
+        acc[i][3] *= a1;
+      }
+    }
+    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;  // nothing seen yet: weights 0
+
+    // weights (bf16; the e4m3 row's scale goes into them) and P V, 16 keys at a time
+    bool odd = false;
+    uint32_t nans = 0;
+#pragma unroll
+    for (int kk = 0; kk < C::TK / 16; ++kk) {
+      uint32_t pa[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float* si = s[2 * kk + u];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) si[e] = ex2_approx(si[e] - (e < 2 ? b0 : b1));
+        l0 += si[0] + si[1];
+        l1 += si[2] + si[3];
+        if constexpr (Q8) {
+          const float fa = pow2_of_byte(__shfl_sync(0xffffffffu, my_ve, (2 * kk + u) * 8 + ka));
+          const float fb = pow2_of_byte(__shfl_sync(0xffffffffu, my_ve, (2 * kk + u) * 8 + kb));
+          si[0] *= fa;
+          si[1] *= fb;
+          si[2] *= fa;
+          si[3] *= fb;
+        }
+        pa[2 * u] = pack_bf16x2(si[0], si[1]);
+        pa[2 * u + 1] = pack_bf16x2(si[2], si[3]);
+      }
+      if constexpr (Q8) {
+        constexpr int W = D / 32;  // words of this thread's columns in a row
+        uint32_t w[4][W];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = kk * 16 + (u >> 1) * 8 + ((u & 1) ? kb : ka);
+          const uint8_t* src = sv + tile_off<D, true>(r, col_of<D>(g) * (D / 8));
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src);
+            w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+          } else if constexpr (D == 64) {
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            w[u][0] = v.x, w[u][1] = v.y;
+          } else {
+            w[u][0] = *reinterpret_cast<const uint32_t*>(src);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          nans |= nan_codes(w[0][i]) | nan_codes(w[1][i]) | nan_codes(w[2][i]) | nan_codes(w[3][i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // byte e of both keys' words, each in the high byte of a half
+            // (what stands in the low bytes is masked away)
+            const uint32_t pick = (e << 4) | ((4u + e) << 12);
+            const uint32_t v0 = e4m3_to_bf16x2(__byte_perm(w[0][i], w[1][i], pick));
+            const uint32_t v1 = e4m3_to_bf16x2(__byte_perm(w[2][i], w[3][i], pick));
+            mma_bf16(acc[4 * i + e], pa, v0, v1);
+          }
+        }
+      } else {
+        const int base = k0 + kk * 16;
+        const bool ra = base + ka < L, rb = base + kb < L, rc = base + 8 + ka < L, rd = base + 8 + kb < L;
+#pragma unroll
+        for (int i = 0; i < D / 8; i += 2) {
+          uint32_t v[4];
+          ldsm4_t(av + tile_off<D, false>(kk * 16 + (lane & 15), (i + (lane >> 4)) * 16), v);
+          if (tail) {
+            v[0] = clean_pair(v[0], ra, rb, odd);
+            v[1] = clean_pair(v[1], rc, rd, odd);
+            v[2] = clean_pair(v[2], ra, rb, odd);
+            v[3] = clean_pair(v[3], rc, rd, odd);
+          }
+          mma_bf16(acc[i], pa, v[0], v[1]);
+          mma_bf16(acc[i + 1], pa, v[2], v[3]);
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, odd || (nans & 0x80808080u) != 0)) {
+      // values left out above that are not finite (bf16: of a tile that some row
+      // sees in part; e4m3: any): only for the rows that see them
+#pragma unroll 1
+      for (int j = 0; j < C::TK; ++j) {
+        const bool v0 = sees(word0, k0 + j, old, L), v1 = sees(word1, k0 + j, old, L);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int col = Q8 ? col_of<D>(2 * t + e) * (D / 8) + i : i * 8 + 2 * t + e;
+            const float v = value_at<D, Q8>(sv, j, col);
+            const bool off = (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u;
+            if (off && v0) acc[i][e] += v;
+            if (off && v1) acc[i][2 + e] += v;
+          }
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && x + C::STAGES < mine) {
+      fence_proxy_async_smem();  // the warp's reads of the stage come before the TMA write
+      load(x + C::STAGES);
+    }
+  }
+  if (x < mine && lane == 0)  // the watchdog fired: let the tiles in flight land
+    for (int y = x; y < x + C::STAGES && y < mine; ++y)
+      tree_drain(&full[warp][y % C::STAGES], (y / C::STAGES) & 1, wd);
+  // join the four warps' results; every load has landed
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+  }
+  // (a row whose every score was NaN has no maximum: its sum is NaN, against the reference 0)
+  if (m0 == -INFINITY && l0 != 0.f) m0 = 0.f;
+  if (m1 == -INFINITY && l1 != 0.f) m1 = 0.f;
+  if (__syncthreads_or(x < mine)) return;
+  float* so = reinterpret_cast<float*>(smem) + warp * (kTreeRows * C::OST);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = Q8 ? col_of<D>(2 * t + e) * (D / 8) + i : i * 8 + 2 * t + e;
+      so[g * C::OST + col] = acc[i][e];
+      so[(g + 8) * C::OST + col] = acc[i][2 + e];
+    }
+  if (t == 0) {
+    s_m[warp][g] = m0;
+    s_m[warp][g + 8] = m1;
+    s_l[warp][g] = l0;
+    s_l[warp][g + 8] = l1;
+  }
+  __syncthreads();
+  const float* sall = reinterpret_cast<const float*>(smem);
+  constexpr int TPR = kTreeThreads / kTreeRows;  // threads of an output row
+  const int r = tid / TPR, row = row0 + r;
+  if (row >= p.rows) return;
+  float M = -INFINITY, l = 0.f, f[kTreeWarps];
+#pragma unroll
+  for (int w = 0; w < kTreeWarps; ++w) M = fmaxf(M, s_m[w][r]);
+#pragma unroll
+  for (int w = 0; w < kTreeWarps; ++w) {
+    f[w] = M == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - M);
+    l = fmaf(f[w], s_l[w][r], l);
+  }
+  auto sum_of = [&](int c) {
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kTreeWarps; ++w) o = fmaf(f[w], sall[(w * kTreeRows + r) * C::OST + c], o);
+    return o;
+  };
+  const size_t out = static_cast<size_t>(bh) * p.rows + row;
+  if (p.splits == 1) {
+    // a row that saw no key is the empty sum
+    const float inv = M == -INFINITY ? 0.f : 1.f / l;
+    for (int c = (tid % TPR) * 2; c < D; c += TPR * 2) {
+      const uint32_t v = pack_bf16x2(sum_of(c) * inv, sum_of(c + 1) * inv);
+      *reinterpret_cast<uint32_t*>(p.o + out * D + c) = v;
+    }
+    if (tid % TPR == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * kTreeLn2;
+  } else {
+    float* part = p.part + ((static_cast<size_t>(bh) * p.splits + split) * p.rows + row) * (D + 2);
+    for (int c = tid % TPR; c < D; c += TPR) part[c] = sum_of(c);
+    if (tid % TPR == 0) {
+      part[D] = M;
+      part[D + 1] = l;
+    }
+  }
+}
+
+// Joins the splits of a row (one warp a row): rescaled to the common maximum
+// and added in split order.
+template <int D>
+__global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p, long long rows, int tk) {
+  const long long out = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (out >= rows) return;
+  const long long bh = out / p.rows;
+  const int row = static_cast<int>(out - bh * p.rows);
+  const int L = head_keys(p.kv_len, static_cast<int>(bh), p.h_kv, p.m);
+  const int per = tiles_per_split(L, tk, p.splits);
+  const int used = per == 0 ? 1 : ((L + tk - 1) / tk + per - 1) / per;  // splits that hold keys
+  const size_t stride = static_cast<size_t>(p.rows) * (D + 2);
+  const float* part = p.part + (static_cast<size_t>(bh) * p.splits * p.rows + row) * (D + 2);
+  float M = -INFINITY;
+  for (int s = lane; s < used; s += 32) M = fmaxf(M, part[s * stride + D]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  constexpr int PER = D / 32;
+  float o[PER], l = 0.f;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) o[u] = 0.f;
+  if (M != -INFINITY) {
+#pragma unroll 4
+    for (int s = 0; s < used; ++s) {
+      const float w = ex2_approx(part[s * stride + D] - M);  // 0 for a split without a key that the row sees
+      l = fmaf(w, part[s * stride + D + 1], l);
+#pragma unroll
+      for (int u = 0; u < PER; ++u)
+        o[u] = fmaf(w, part[s * stride + lane + 32 * u], o[u]);
+    }
+  }
+  const float inv = M == -INFINITY ? 0.f : 1.f / l;
+  __nv_bfloat16* orow = p.o + static_cast<size_t>(out) * D;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) orow[lane + 32 * u] = __float2bfloat16_rn(o[u] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * kTreeLn2;
+}
+
+template <int D, bool Q8>
+cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, int BH,
+                          cudaStream_t stream) {
+  using C = Tree<D, Q8>;
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!set[dev & 63].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(attn_tree_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(C::SMEM));
+    if (e != cudaSuccess) return e;
+    set[dev & 63].store(true, std::memory_order_relaxed);
+  }
+  prof_begin(kKindTree, stream);
+  attn_tree_kernel<D, Q8><<<dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>(BH),
+                                 static_cast<unsigned>((p.rows + kTreeRows - 1) / kTreeRows)),
+                            kTreeThreads, C::SMEM, stream>>>(tk, tv, p);
+  e = cudaGetLastError();
+  prof_end(kKindTree, stream);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const long long rows = static_cast<long long>(BH) * p.rows;
+  prof_begin(kKindTreeMerge, stream);
+  attn_tree_merge_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p, rows, C::TK);
+  e = cudaGetLastError();
+  prof_end(kKindTreeMerge, stream);
+  return e;
+}
+
+}  // namespace
+
+int tree_tile(int d, bool quantised) { return (d == 128 && !quantised) ? 16 : 32; }
+
+int tree_splits(long long BH, int rows, int m, int d, bool quantised) {
+  const long long ctas = BH * ((rows + kTreeRows - 1) / kTreeRows);
+  const long long tiles = (m + tree_tile(d, quantised) - 1) / tree_tile(d, quantised);
+  long long splits = (8ll * kSms + ctas - 1) / ctas;
+  const long long most = (tiles + 2 * kTreeWarps - 1) / (2 * kTreeWarps);  // at least two tiles a warp
+  if (splits > most) splits = most;
+  return static_cast<int>(splits < 1 ? 1 : splits);
+}
+
+cudaError_t launch_tree(int d, bool quantised, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                        int BH, cudaStream_t stream) {
+  switch (d) {
+    case 32: return quantised ? launch_tree_d<32, true>(tk, tv, p, BH, stream) : launch_tree_d<32, false>(tk, tv, p, BH, stream);
+    case 64: return quantised ? launch_tree_d<64, true>(tk, tv, p, BH, stream) : launch_tree_d<64, false>(tk, tv, p, BH, stream);
+    case 128: return quantised ? launch_tree_d<128, true>(tk, tv, p, BH, stream) : launch_tree_d<128, false>(tk, tv, p, BH, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace attn

@@ -146,6 +146,31 @@ def test_far_offsets():
             assert ((o[0, hd, i].cpu().double() - ref).abs() <= 2.0 ** -6 * (w @ vv[:i + 1].abs()) / total).all()
 
 
+@pytest.mark.parametrize("rows", [1, 40, 200])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_every_code_as_a_value(d, rows):
+    """A step that sees one position returns that position's value row: every finite code,
+    at small, ordinary and large exponents, through each of the tree step's kernels."""
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes = codes[(codes & 0x7f) != 0x7f]
+    codes = torch.cat([codes, codes[:2 * d - len(codes) % d - (d if len(codes) % d == 0 else 0)]])
+    codes = codes[:len(codes) // d * d].reshape(-1, d)
+    for byte in (127 - 117, 100, 127, 135, 136, 246):
+        B = codes.shape[0]
+        n = min(rows, 64)
+        h = (rows + n - 1) // n
+        kc = torch.zeros(B, 1, n, d, dtype=torch.uint8)
+        vc = kc.clone()
+        vc[:, 0, 0] = codes
+        e = torch.full((B, 1, n), byte, dtype=torch.uint8)
+        q = R.bf16(B, h, n, d, seed=3)
+        tree = torch.ones(B, n, dtype=torch.int64)  # every query sees position 0 alone
+        o, _ = A.attn_decode_tree(q.to(DEV), kc.to(DEV).view(E4M3), vc.to(DEV).view(E4M3), tree=tree.to(DEV),
+                                  k_exp=e.to(DEV), v_exp=e.to(DEV))
+        want = codes.view(E4M3).float().double() * 2.0 ** (byte - 127)
+        assert torch.equal(o.cpu().double(), want[:, None, None].expand(B, h, n, d))
+
+
 def test_captured_and_replayed():
     B, h, n, m, d = 2, 2, 3, 40, 64
     k, v = R.bf16(B, h, n, d, seed=1).to(DEV), R.bf16(B, h, n, d, seed=2).to(DEV)

@@ -1049,18 +1049,21 @@ static int check_tree(int B, int h, int h_kv, int n, int m, int d) {
   if (d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (h_kv == 0 ? h != 0 : h % h_kv != 0) return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * h_kv > 65535 || static_cast<long long>(h) * n > 0xfffffLL)
-    return ATTN_ERR_UNSUPPORTED;  // grid y, z
+    return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
+}
+
+static size_t tree_workspace(const attn::TreePlan& l, int d) {
+  return l.grid <= 1 ? 0 : static_cast<size_t>(l.slots) * l.block_rows * (static_cast<size_t>(d) + 2) * sizeof(float);
 }
 
 size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int m, int d) {
   if (check_tree(B, h, h_kv, n, m, d) != ATTN_OK || B == 0 || h == 0) return 0;
-  const long long BH = static_cast<long long>(B) * h_kv;
   const int rows = h / h_kv * n;
   // enough for either cache type
-  const int a = attn::tree_splits(BH, rows, m, d, false), b = attn::tree_splits(BH, rows, m, d, true);
-  const int splits = a > b ? a : b;
-  return splits == 1 ? 0 : static_cast<size_t>(BH) * splits * rows * (static_cast<size_t>(d) + 2) * sizeof(float);
+  const size_t a = tree_workspace(attn::tree_plan(B, h_kv, rows, m, d, false), d);
+  const size_t b = tree_workspace(attn::tree_plan(B, h_kv, rows, m, d, true), d);
+  return a > b ? a : b;
 }
 
 int attn_decode_tree(const void* q, const void* k, const void* v, void* o, float* lse, const void* k_exp,
@@ -1074,15 +1077,18 @@ int attn_decode_tree(const void* q, const void* k, const void* v, void* o, float
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
   if (!aligned4(lse) || !aligned4(kv_len) || (reinterpret_cast<uintptr_t>(tree) & 7u) != 0)
     return ATTN_ERR_INVALID_ARG;
-  const size_t need = attn_decode_tree_workspace_bytes(B, h, h_kv, n, m, d);
+  const bool quantised = k_exp != nullptr;
+  const int rows = h / h_kv * n;
+  const attn::TreePlan plan = attn::tree_plan(B, h_kv, rows, m, d, quantised);
+  const size_t need = tree_workspace(plan, d);
   if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
   const long long BH = static_cast<long long>(B) * h_kv;
-  const bool quantised = k_exp != nullptr;
-  const int tile = attn::tree_tile(d, quantised);
-  CUtensorMap tk, tv;
-  if (quantised ? (!make_code_map(&tk, k, BH, m, d, tile) || !make_code_map(&tv, v, BH, m, d, tile))
-                : (!make_tile_map(&tk, k, BH, m, d, tile) || !make_tile_map(&tv, v, BH, m, d, tile)))
+  const int box = plan.tc ? 128 : plan.tile / 4;  // a warp's keys, or a whole tile
+  CUtensorMap tq, tk, tv;
+  if (quantised ? (!make_code_map(&tk, k, BH, m, d, box) || !make_code_map(&tv, v, BH, m, d, box))
+                : (!make_tile_map(&tk, k, BH, m, d, box) || !make_tile_map(&tv, v, BH, m, d, box)))
     return ATTN_ERR_CUDA;
+  if (plan.tc && !make_tile_map(&tq, q, BH, rows, d)) return ATTN_ERR_CUDA;
   uint32_t* status = nullptr;
   if (device_status_word(&status) != cudaSuccess) return ATTN_ERR_CUDA;
   attn::TreeParams p{};
@@ -1090,20 +1096,25 @@ int attn_decode_tree(const void* q, const void* k, const void* v, void* o, float
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.part = static_cast<float*>(workspace);
+  p.part_ml = p.part + static_cast<size_t>(plan.slots) * plan.block_rows * d;
   p.tree = reinterpret_cast<const unsigned long long*>(tree);
   p.kv_len = kv_len;
+  p.k = k;
+  p.v = v;
   p.k_exp = static_cast<const unsigned char*>(k_exp);
   p.v_exp = static_cast<const unsigned char*>(v_exp);
+  p.B = B;
   p.h_kv = h_kv;
   p.n = n;
-  p.rows = h / h_kv * n;
+  p.rows = rows;
   p.m = m;
-  p.splits = attn::tree_splits(BH, p.rows, m, d, quantised);
+  p.row_blocks = plan.row_blocks;
+  p.block_rows = plan.block_rows;
+  p.neg = scale < 0.f ? 1 : 0;
   p.c = static_cast<float>(static_cast<double>(scale) * kLog2e);
   p.wd.status = status;
   p.wd.budget_ns = g_watchdog_ns.load();
-  const cudaError_t e = attn::launch_tree(d, quantised, tk, tv, p, static_cast<int>(BH),
-                                          reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = attn::launch_tree(d, quantised, plan, tq, tk, tv, p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

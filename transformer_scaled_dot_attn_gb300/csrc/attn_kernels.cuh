@@ -302,18 +302,32 @@ struct TreeParams {
   const __nv_bfloat16* q;          // [B h_kv][rows][d]: the query heads of a key head are neighbours
   __nv_bfloat16* o;                // like q
   float* lse;                      // [B h_kv][rows] or nullptr
-  float* part;                     // [B h_kv][splits][rows][d + 2] fp32 partials
+  float* part;                     // [slots][block rows][d] fp32 partial O (not divided)
+  float* part_ml;                  // [slots][block rows][2]: maximum (log2 units) and sum
   const unsigned long long* tree;  // [B][n] or nullptr (causal)
   const int* kv_len;               // [B] or nullptr
+  const void *k, *v;               // the caches (the tiles come through tensor maps)
   const unsigned char *k_exp, *v_exp;  // [B h_kv][m] (e4m3 caches)
-  int h_kv, n, rows, m, splits;    // rows = (h / h_kv) n
+  int B, h_kv, n, rows, m;         // rows = (h / h_kv) n
+  int row_blocks, block_rows;      // query rows of a key head in blocks of block_rows
+  int neg;                         // tensor-core kernel: scale < 0, and c = |scale| log2(e)
   float c;                         // scale log2(e)
   Watchdog wd;
 };
-// Rows the key tiles' TMA box holds, for the cache type and head size.
-int tree_tile(int d, bool quantised);
-int tree_splits(long long BH, int rows, int m, int d, bool quantised);
-cudaError_t launch_tree(int d, bool quantised, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
-                        int BH, cudaStream_t stream);
+
+// How a step is run: fixed by its sizes and cache type.
+struct TreePlan {
+  bool tc;                 // the tcgen05 kernel (128-row query tiles), else mma.sync (16 rows)
+  int tile;                // keys of a TMA box
+  int row_blocks, block_rows;
+  int grid;                // CTAs
+  long long slots;         // partial results
+};
+TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised);
+cudaError_t launch_tree(int d, bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
+// The tcgen05 kernel (attn_tree_tc.cu).
+cudaError_t launch_tree_tc(int d, bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
+                           const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
 
 }  // namespace attn

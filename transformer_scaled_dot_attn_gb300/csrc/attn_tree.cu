@@ -18,7 +18,8 @@
 // mma.sync with 16 query rows (a tcgen05 tile has 128 rows, most of them idle
 // here, and its operands would have to be written out in 16 bits first). The
 // warps' results are joined in shared memory, the CTAs' by a second kernel.
-#include "attn_kernels.cuh"
+// Many rows take the tcgen05 kernel (attn_tree_tc.cu).
+#include "attn_tree.cuh"
 
 #include <atomic>
 
@@ -29,8 +30,9 @@ using namespace sm103;
 
 constexpr int kTreeWarps = 4;
 constexpr int kTreeThreads = kTreeWarps * 32;
-constexpr int kTreeRows = 16;  // query rows of a CTA (one mma.sync tile)
-constexpr float kTreeLn2 = 0.69314718055994530942f;
+constexpr int kTreeRows = 16;     // query rows of a CTA (one mma.sync tile)
+constexpr int kTreeLeast = 2;     // tiles (of four warps) worth a CTA of their own
+constexpr int kTreeLeastTc = 2;   // the same for the tcgen05 kernel
 
 template <int D, bool Q8>
 struct Tree {
@@ -40,7 +42,9 @@ struct Tree {
   static constexpr uint32_t ROWB = D * ES <= 128 ? D * ES : 128;  // bytes of a row in a TMA box
   static constexpr uint32_t BOX = TK * ROWB;
   static constexpr int NBOX = D * ES / ROWB;
+  static constexpr int BN = kTreeWarps * TK;               // keys of a CTA's tile
   static constexpr int STAGES = 3;
+  static constexpr int CTAS = D == 128 ? 2 : 4;            // per SM
   static constexpr int NT = TK / 8;                        // n8 score tiles
   static constexpr int KS = D / 16;                        // k steps of the score product
   static constexpr uint32_t RING = kTreeWarps * STAGES * 2 * KT;
@@ -77,20 +81,9 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// Two e4m3 codes (the halves' high bytes) as a bf16 pair: the code's exponent
-// and significand moved to bf16's places stand for its value times 2^-120
-// (bias 7 against 127; subnormal codes included), which one exact product
-// undoes. The NaN code comes out as 480 here; nan_codes finds it.
 __device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t high_bytes) {
-  const uint32_t x = ((high_bytes >> 4) & 0x07f007f0u) | (high_bytes & 0x80008000u);
-  const uint32_t up = 0x7b807b80u;  // 2^120, twice
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(up));
-  return r;
+  return mul_bf16x2(e4m3_places(high_bytes), 0x7b807b80u);  // 2^120, twice
 }
-
-// Bit 7 of a byte of the result is set where that code is NaN (0x7f, 0xff).
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 
 __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
   uint32_t r;
@@ -158,26 +151,6 @@ __device__ __forceinline__ void tree_drain(uint64_t* bar, uint32_t parity, const
   }
 }
 
-__device__ __forceinline__ float pow2_of_byte(int byte) {
-  return __uint_as_float(byte == 0 ? 0x00400000u : static_cast<uint32_t>(byte) << 23);
-}
-
-// Key tiles a split of a sequence with L cached positions takes.
-__device__ __forceinline__ int tiles_per_split(int L, int tk, int splits) {
-  return ((L + tk - 1) / tk + splits - 1) / splits;
-}
-
-// The newest positions a query sees: bit t stands for position L - n + t.
-__device__ __forceinline__ unsigned long long tree_word(const TreeParams& p, int b, int row) {
-  const int i = row % p.n;
-  if (p.tree != nullptr) return __ldg(p.tree + static_cast<size_t>(b) * p.n + i);
-  return i >= 63 ? ~0ull : (1ull << (i + 1)) - 1ull;
-}
-
-__device__ __forceinline__ bool sees(unsigned long long word, int key, int old, int L) {
-  return key < L && (key < old || ((word >> (key - old)) & 1ull));
-}
-
 template <int D, bool Q8>
 __device__ __forceinline__ float value_at(const uint8_t* tile, int r, int c) {
   if constexpr (Q8) {
@@ -208,9 +181,10 @@ __device__ __forceinline__ uint32_t clean_pair(uint32_t v, bool lo_real, bool hi
   return v;
 }
 
-// Grid: x = key split, y = (sequence, key head), z = block of 16 query rows.
+// One CTA per share of the line of tiles (attn_tree.cuh); a tile is the four
+// warps' TK keys each.
 template <int D, bool Q8>
-__global__ void __launch_bounds__(kTreeThreads)
+__global__ void __launch_bounds__(kTreeThreads, Tree<D, Q8>::CTAS)
 attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const TreeParams p) {
   using C = Tree<D, Q8>;
@@ -222,15 +196,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                                              ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x, bh = blockIdx.y, row0 = blockIdx.z * kTreeRows;
-  const int b = bh / p.h_kv;
-  const int L = head_keys(p.kv_len, bh, p.h_kv, p.m);
-  const int old = L - p.n;  // positions before the newest n (negative: fewer cached than n)
-  const int per = tiles_per_split(L, C::TK, p.splits);
-  const int tile0 = split * per, tile1 = min((L + C::TK - 1) / C::TK, tile0 + per);
-  if (tile0 >= tile1 && split > 0) return;  // split 0 also stands for an empty cache
   volatile int* abort_flag = &abort_word;
   const Watchdog wd = p.wd;
+  TreeWalk walk;
+  if (!tree_start(p, C::BN, kTreeLeast, walk)) return;
   if (tid == 0) {
     for (int w = 0; w < kTreeWarps; ++w)
       for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[w][s], 1);
@@ -240,13 +209,19 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     prefetch_tensormap(&tm_v);
   }
   __syncthreads();
-
-  // this warp's tiles: tile0 + warp, then every fourth
-  const int mine = tile1 - tile0 > warp ? (tile1 - tile0 - warp + kTreeWarps - 1) / kTreeWarps : 0;
   uint8_t* ring = smem + warp * (C::STAGES * 2 * C::KT);
+  int turn = 0;  // tiles this warp has put through its ring
+  TreePart part;
+#pragma unroll 1
+  while (tree_next(p, C::BN, walk, part)) {
+  const int bh = part.bh, b = part.b, row0 = part.rb * kTreeRows;
+  const int L = part.L;
+  const int old = L - p.n;  // positions before the newest n (negative: fewer cached than n)
+  const int mine = part.t1 - part.t0;  // of every tile this warp takes keys [warp TK, warp TK + TK)
+  const int key0 = part.t0 * C::BN + warp * C::TK;
   auto load = [&](int x) {
-    const int st = x % C::STAGES;
-    const int k0 = (tile0 + warp + x * kTreeWarps) * C::TK;
+    const int st = (turn + x) % C::STAGES;
+    const int k0 = key0 + x * C::BN;
     uint8_t* dst = ring + st * 2 * C::KT;
     mbar_arrive_expect_tx(&full[warp][st], 2 * C::KT);
     for (int a = 0; a < C::NBOX; ++a) {
@@ -324,7 +299,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   // e4m3: lane j holds the scale bytes of key j of the tile, read one tile ahead
   int ke = 127, ve = 127;
   auto scales = [&](int x) {
-    const int key = (tile0 + warp + x * kTreeWarps) * C::TK + lane;
+    const int key = key0 + x * C::BN + lane;
     const bool in = x < mine && key < L;
     const size_t at = static_cast<size_t>(bh) * p.m + key;
     ke = in ? __ldg(p.k_exp + at) : 127;
@@ -334,14 +309,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 
   int x = 0;
   for (; x < mine; ++x) {
-    const int st = x % C::STAGES;
-    const int k0 = (tile0 + warp + x * kTreeWarps) * C::TK;
+    const int st = (turn + x) % C::STAGES;
+    const int k0 = key0 + x * C::BN;
     const uint8_t* sk = ring + st * 2 * C::KT;
     const uint8_t* sv = sk + C::KT;
     const uint32_t ak = smem_u32(sk), av = smem_u32(sv);
     const int my_ke = ke, my_ve = ve;
     if constexpr (Q8) scales(x + 1);
-    if (!__all_sync(0xffffffffu, tree_wait(&full[warp][st], (x / C::STAGES) & 1, abort_flag, wd))) break;
+    if (!__all_sync(0xffffffffu, tree_wait(&full[warp][st], ((turn + x) / C::STAGES) & 1, abort_flag, wd))) break;
 
     // scores of the tile's keys
     float s[C::NT][4];
@@ -523,7 +498,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   }
   if (x < mine && lane == 0)  // the watchdog fired: let the tiles in flight land
     for (int y = x; y < x + C::STAGES && y < mine; ++y)
-      tree_drain(&full[warp][y % C::STAGES], (y / C::STAGES) & 1, wd);
+      tree_drain(&full[warp][(turn + y) % C::STAGES], ((turn + y) / C::STAGES) & 1, wd);
   // join the four warps' results; every load has landed
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
@@ -553,7 +528,6 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const float* sall = reinterpret_cast<const float*>(smem);
   constexpr int TPR = kTreeThreads / kTreeRows;  // threads of an output row
   const int r = tid / TPR, row = row0 + r;
-  if (row >= p.rows) return;
   float M = -INFINITY, l = 0.f, f[kTreeWarps];
 #pragma unroll
   for (int w = 0; w < kTreeWarps; ++w) M = fmaxf(M, s_m[w][r]);
@@ -568,67 +542,97 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     for (int w = 0; w < kTreeWarps; ++w) o = fmaf(f[w], sall[(w * kTreeRows + r) * C::OST + c], o);
     return o;
   };
-  const size_t out = static_cast<size_t>(bh) * p.rows + row;
-  if (p.splits == 1) {
-    // a row that saw no key is the empty sum
-    const float inv = M == -INFINITY ? 0.f : 1.f / l;
-    for (int c = (tid % TPR) * 2; c < D; c += TPR * 2) {
-      const uint32_t v = pack_bf16x2(sum_of(c) * inv, sum_of(c + 1) * inv);
-      *reinterpret_cast<uint32_t*>(p.o + out * D + c) = v;
+  if (row < p.rows) {
+    const float inv = M == -INFINITY ? 0.f : 1.f / l;  // a row that saw no key is the empty sum
+    if (part.whole) {
+      const size_t out = static_cast<size_t>(bh) * p.rows + row;
+      for (int c = (tid % TPR) * 2; c < D; c += TPR * 2) {
+        const uint32_t v = pack_bf16x2(sum_of(c) * inv, sum_of(c + 1) * inv);
+        *reinterpret_cast<uint32_t*>(p.o + out * D + c) = v;
+      }
+      if (tid % TPR == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * kTreeLn2;
+    } else {
+      const size_t at = static_cast<size_t>(part.slot) * p.block_rows + r;
+      for (int c = (tid % TPR) * 2; c < D; c += TPR * 2)
+        *reinterpret_cast<float2*>(p.part + at * D + c) = make_float2(sum_of(c), sum_of(c + 1));
+      if (tid % TPR == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(M, l);
     }
-    if (tid % TPR == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * kTreeLn2;
-  } else {
-    float* part = p.part + ((static_cast<size_t>(bh) * p.splits + split) * p.rows + row) * (D + 2);
-    for (int c = tid % TPR; c < D; c += TPR) part[c] = sum_of(c);
-    if (tid % TPR == 0) {
-      part[D] = M;
-      part[D + 1] = l;
-    }
+  }
+  turn += mine;
+  fence_proxy_async_smem();  // the results in the ring come before the next part's TMA writes
+  __syncthreads();
   }
 }
 
-// Joins the splits of a row (one warp a row): rescaled to the common maximum
-// and added in split order.
+// Joins the parts of a unit's rows (one warp a row), rescaled to the common
+// maximum and added in the line's order. Grid: x = unit, y = 8 rows of its block.
 template <int D>
-__global__ void __launch_bounds__(128) attn_tree_merge_kernel(const TreeParams p, long long rows, int tk) {
-  const long long out = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (out >= rows) return;
-  const long long bh = out / p.rows;
-  const int row = static_cast<int>(out - bh * p.rows);
-  const int L = head_keys(p.kv_len, static_cast<int>(bh), p.h_kv, p.m);
-  const int per = tiles_per_split(L, tk, p.splits);
-  const int used = per == 0 ? 1 : ((L + tk - 1) / tk + per - 1) / per;  // splits that hold keys
-  const size_t stride = static_cast<size_t>(p.rows) * (D + 2);
-  const float* part = p.part + (static_cast<size_t>(bh) * p.splits * p.rows + row) * (D + 2);
+__global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p, int bn, int grid, int least) {
+  const TreeLine l = tree_line(p, bn, grid, least);
+  const int unit = blockIdx.x, lane = threadIdx.x & 31;
+  const int b = unit / l.per_seq, idx = unit - b * l.per_seq;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int row = (idx % p.row_blocks) * p.block_rows + r;
+  if (r >= p.block_rows || row >= p.rows) return;
+  long long first = 0;  // the unit's place on the line
+  const int tiles = tiles_of(tree_len(p, b), bn);
+  if (p.kv_len == nullptr) {
+    first = static_cast<long long>(b) * tiles;
+  } else {
+    for (int x = lane; x < b; x += 32) first += tiles_of(tree_len(p, x), bn);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+  }
+  first = first * l.per_seq + static_cast<long long>(idx) * tiles;
+  // the CTAs that hold its first and its last tile: the largest c with U c / ctas at or before them
+  const int c0 = static_cast<int>(((first + 1) * l.ctas - 1) / l.U);
+  const int c1 = static_cast<int>(((first + tiles) * l.ctas - 1) / l.U);
+  if (c0 == c1) return;  // one part: its CTA wrote the results
+  const size_t step = static_cast<size_t>(p.block_rows);
+  const size_t at = (static_cast<size_t>(unit) + c0) * step + r;
+  const int parts = c1 - c0 + 1;
   float M = -INFINITY;
-  for (int s = lane; s < used; s += 32) M = fmaxf(M, part[s * stride + D]);
+  for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[2 * (at + s * step)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   constexpr int PER = D / 32;
-  float o[PER], l = 0.f;
+  float o[PER], sum = 0.f;
 #pragma unroll
   for (int u = 0; u < PER; ++u) o[u] = 0.f;
   if (M != -INFINITY) {
 #pragma unroll 4
-    for (int s = 0; s < used; ++s) {
-      const float w = ex2_approx(part[s * stride + D] - M);  // 0 for a split without a key that the row sees
-      l = fmaf(w, part[s * stride + D + 1], l);
+    for (int s = 0; s < parts; ++s) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + s * step));
+      const float w = ex2_approx(ml.x - M);  // 0 for a part without a key that the row sees
+      sum = fmaf(w, ml.y, sum);
 #pragma unroll
-      for (int u = 0; u < PER; ++u)
-        o[u] = fmaf(w, part[s * stride + lane + 32 * u], o[u]);
+      for (int u = 0; u < PER; ++u) o[u] = fmaf(w, p.part[(at + s * step) * D + lane + 32 * u], o[u]);
     }
   }
-  const float inv = M == -INFINITY ? 0.f : 1.f / l;
-  __nv_bfloat16* orow = p.o + static_cast<size_t>(out) * D;
+  const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+  const size_t out = (static_cast<size_t>(b) * p.h_kv + idx / p.row_blocks) * p.rows + row;
 #pragma unroll
-  for (int u = 0; u < PER; ++u) orow[lane + 32 * u] = __float2bfloat16_rn(o[u] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * kTreeLn2;
+  for (int u = 0; u < PER; ++u) p.o[out * D + lane + 32 * u] = __float2bfloat16_rn(o[u] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
+}
+
+int small_ctas(int d, bool quantised) {
+  switch (d) {
+    case 32: return quantised ? Tree<32, true>::CTAS : Tree<32, false>::CTAS;
+    case 64: return quantised ? Tree<64, true>::CTAS : Tree<64, false>::CTAS;
+    default: return quantised ? Tree<128, true>::CTAS : Tree<128, false>::CTAS;
+  }
+}
+
+bool tree_uses_tc(int rows, int d, bool quantised) {
+  (void)d;
+  (void)quantised;
+  return rows > 32;
 }
 
 template <int D, bool Q8>
-cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, int BH,
-                          cudaStream_t stream) {
+cudaError_t launch_small(int grid, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                         cudaStream_t stream) {
   using C = Tree<D, Q8>;
   static std::atomic<bool> set[64];
   int dev = 0;
@@ -641,15 +645,25 @@ cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const Tr
     set[dev & 63].store(true, std::memory_order_relaxed);
   }
   prof_begin(kKindTree, stream);
-  attn_tree_kernel<D, Q8><<<dim3(static_cast<unsigned>(p.splits), static_cast<unsigned>(BH),
-                                 static_cast<unsigned>((p.rows + kTreeRows - 1) / kTreeRows)),
-                            kTreeThreads, C::SMEM, stream>>>(tk, tv, p);
+  attn_tree_kernel<D, Q8><<<static_cast<unsigned>(grid), kTreeThreads, C::SMEM, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   prof_end(kKindTree, stream);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  const long long rows = static_cast<long long>(BH) * p.rows;
+  return e;
+}
+
+template <int D>
+cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
+                          const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
+  cudaError_t e;
+  if (plan.tc) e = launch_tree_tc(D, quantised, plan.grid, kTreeLeastTc, tq, tk, tv, p, stream);
+  else if (quantised) e = launch_small<D, true>(plan.grid, tk, tv, p, stream);
+  else e = launch_small<D, false>(plan.grid, tk, tv, p, stream);
+  if (e != cudaSuccess || plan.grid == 1) return e;
+  const unsigned units = static_cast<unsigned>(p.B) * p.h_kv * p.row_blocks;
+  const int warps = p.block_rows < 8 ? p.block_rows : 8;
   prof_begin(kKindTreeMerge, stream);
-  attn_tree_merge_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p, rows, C::TK);
+  attn_tree_merge_kernel<D><<<dim3(units, static_cast<unsigned>((p.block_rows + 7) / 8)), warps * 32, 0, stream>>>(
+      p, plan.tile, plan.grid, plan.tc ? kTreeLeastTc : kTreeLeast);
   e = cudaGetLastError();
   prof_end(kKindTreeMerge, stream);
   return e;
@@ -657,23 +671,34 @@ cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const Tr
 
 }  // namespace
 
-int tree_tile(int d, bool quantised) { return (d == 128 && !quantised) ? 16 : 32; }
-
-int tree_splits(long long BH, int rows, int m, int d, bool quantised) {
-  const long long ctas = BH * ((rows + kTreeRows - 1) / kTreeRows);
-  const long long tiles = (m + tree_tile(d, quantised) - 1) / tree_tile(d, quantised);
-  long long splits = (8ll * kSms + ctas - 1) / ctas;
-  const long long most = (tiles + 2 * kTreeWarps - 1) / (2 * kTreeWarps);  // at least two tiles a warp
-  if (splits > most) splits = most;
-  return static_cast<int>(splits < 1 ? 1 : splits);
+TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised) {
+  TreePlan l{};
+  l.tc = tree_uses_tc(rows, d, quantised);
+  if (l.tc) {
+    l.block_rows = rows <= 128 ? 128 : 256;
+    l.tile = 128;
+  } else {
+    l.block_rows = rows < kTreeRows ? rows : kTreeRows;
+    l.tile = kTreeWarps * ((d == 128 && !quantised) ? 16 : 32);
+  }
+  l.row_blocks = (rows + l.block_rows - 1) / l.block_rows;
+  const long long units = static_cast<long long>(B) * h_kv * l.row_blocks;
+  // one CTA for each place on the GPU's SMs; fewer where the caches (at their
+  // capacity) hold too few tiles
+  const int least = l.tc ? kTreeLeastTc : kTreeLeast;
+  const long long most = (units * ((m + l.tile - 1) / l.tile) + least - 1) / least;
+  const long long room = static_cast<long long>(kSms) * (l.tc ? 1 : small_ctas(d, quantised));
+  l.grid = static_cast<int>(most < room ? most : room);
+  l.slots = units + l.grid;
+  return l;
 }
 
-cudaError_t launch_tree(int d, bool quantised, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
-                        int BH, cudaStream_t stream) {
+cudaError_t launch_tree(int d, bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   switch (d) {
-    case 32: return quantised ? launch_tree_d<32, true>(tk, tv, p, BH, stream) : launch_tree_d<32, false>(tk, tv, p, BH, stream);
-    case 64: return quantised ? launch_tree_d<64, true>(tk, tv, p, BH, stream) : launch_tree_d<64, false>(tk, tv, p, BH, stream);
-    case 128: return quantised ? launch_tree_d<128, true>(tk, tv, p, BH, stream) : launch_tree_d<128, false>(tk, tv, p, BH, stream);
+    case 32: return launch_tree_d<32>(quantised, plan, tq, tk, tv, p, stream);
+    case 64: return launch_tree_d<64>(quantised, plan, tq, tk, tv, p, stream);
+    case 128: return launch_tree_d<128>(quantised, plan, tq, tk, tv, p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

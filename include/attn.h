@@ -408,8 +408,8 @@ int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* w_q, const v
  *   (every value is a bf16 number); rows at or past kv_len[b] (NULL: m) become
  *   zeros, so attn_fwd_varlen can take the result.
  * Tensors 16-byte aligned, lengths int32 device arrays; d in {32, 64, 128}.
- * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED (other d, more
- * than 2^34 rows) or ATTN_ERR_CUDA. Asynchronous on `stream`; profiling kind 8.
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED (other d, 2^32
+ * rows or more) or ATTN_ERR_CUDA. Asynchronous on `stream`; profiling kind 8.
  */
 int attn_cache_write(const void* k, const void* v, void* k_cache, void* v_cache, void* k_exp, void* v_exp,
                      const int* kv_len, const int* new_len, int B, int h_kv, int n, int m, int d,

@@ -943,8 +943,8 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int B, int h, int h_kv, int n, int 
   const long long heads = static_cast<long long>(h) + h_kv;
   if (heads < 1 || heads > 65535) return 0;
   int gx = 0, gy = 0, per = 0;
-  attn::norm_rope_bwd_grid(d, static_cast<long long>(B) * n, static_cast<int>(heads), &gx, &gy, &per);
-  return static_cast<size_t>(gx) * gy * 2 * d * sizeof(float);
+  attn::norm_rope_bwd_grid(d, static_cast<long long>(B) * n, h, h_kv, &gx, &gy, &per);
+  return static_cast<size_t>(gx) * gy * d * sizeof(float);
 }
 
 int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* w_q, const void* w_k, const int* positions,
@@ -984,7 +984,7 @@ int attn_qk_norm_rope_bwd(const void* q, const void* k, const void* w_q, const v
 static int check_cache(int B, int h_kv, int m, int d, long long rows, const int* kv_len) {
   if (B < 0 || h_kv < 0 || m < 1) return ATTN_ERR_INVALID_ARG;
   if (d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * h_kv > 0x7fffffffLL || rows > (1ll << 34)) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * h_kv > 0x7fffffffLL || rows > 0xffffffffLL) return ATTN_ERR_UNSUPPORTED;
   if (!aligned4(kv_len)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -994,7 +994,7 @@ int attn_cache_write(const void* k, const void* v, void* k_cache, void* v_cache,
                      attn_stream_t stream) {
   if (n < 0) return ATTN_ERR_INVALID_ARG;
   const long long BH = static_cast<long long>(B) * h_kv;
-  if (n > 0 && BH > (1ll << 34) / n) return ATTN_ERR_UNSUPPORTED;
+  if (n > 0 && BH > 0xffffffffLL / n) return ATTN_ERR_UNSUPPORTED;
   const int st = check_cache(B, h_kv, m, d, BH * n, kv_len);
   if (st != ATTN_OK) return st;
   if (!aligned4(new_len)) return ATTN_ERR_INVALID_ARG;
@@ -1022,7 +1022,7 @@ int attn_cache_write(const void* k, const void* v, void* k_cache, void* v_cache,
 int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_exp, const void* v_exp, void* k, void* v,
                     const int* kv_len, int B, int h_kv, int m, int d, attn_stream_t stream) {
   const long long BH = static_cast<long long>(B) * h_kv;
-  if (m > 0 && BH > (1ll << 34) / m) return ATTN_ERR_UNSUPPORTED;
+  if (m > 0 && BH > 0xffffffffLL / m) return ATTN_ERR_UNSUPPORTED;
   const int st = check_cache(B, h_kv, m, d, BH * m, kv_len);
   if (st != ATTN_OK) return st;
   if (BH == 0) return ATTN_OK;
@@ -1054,7 +1054,7 @@ static int check_tree(int B, int h, int h_kv, int n, int m, int d) {
 }
 
 static size_t tree_workspace(const attn::TreePlan& l, int d) {
-  return l.grid <= 1 ? 0 : static_cast<size_t>(l.slots) * l.block_rows * (static_cast<size_t>(d) + 2) * sizeof(float);
+  return l.by_unit ? 0 : static_cast<size_t>(l.slots) * l.block_rows * (static_cast<size_t>(d) + 2) * sizeof(float);
 }
 
 size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int m, int d) {
@@ -1110,7 +1110,7 @@ int attn_decode_tree(const void* q, const void* k, const void* v, void* o, float
   p.m = m;
   p.row_blocks = plan.row_blocks;
   p.block_rows = plan.block_rows;
-  p.neg = scale < 0.f ? 1 : 0;
+  p.by_unit = plan.by_unit ? 1 : 0;
   p.c = static_cast<float>(static_cast<double>(scale) * kLog2e);
   p.wd.status = status;
   p.wd.budget_ns = g_watchdog_ns.load();

@@ -253,6 +253,28 @@ int proj_bwd_splits(int M, int N, int chunks);
 // out (bf16) = sum over splits of part[z][0 .. count), count a multiple of 8.
 cudaError_t launch_proj_reduce(const float* part, void* out, long long count, int splits, cudaStream_t stream);
 
+// Programmatic dependent launch: a kernel that joins partial results is
+// started while the one that writes them still runs (its blocks wait in
+// grid_wait until those writes are visible), which hides its launch.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---------------------------------------------------------------- norm + rotation
 
 constexpr int kSms = 152;  // SMs of the GPU this library is built for (grid sizes only)
@@ -266,16 +288,17 @@ struct NormRopeParams {
   const __nv_bfloat16 *dq_out, *dk_out;  // backward: upstream gradients
   __nv_bfloat16 *dq, *dk;              // backward: input gradients
   __nv_bfloat16 *dw_q, *dw_k;          // backward: weight gradients [d]
-  float* part;                         // backward: fp32 partials [blocks][2][d]
+  float* part;                         // backward: fp32 partials [blocks][d]
   long long tokens;                    // B n
   long long token_blocks;              // set by the launcher
   int n, h, h_kv, rot, axes;
   int sec0, sec1;                      // pairs from sec0 (sec1) on turn by axis 1 (2)
   int interleaved;
   int heads_per;                       // heads a block loops over; set by the launcher
+  int q_chunks;                        // backward: chunks of query heads; set by the launcher
   float eps;
 };
-void norm_rope_bwd_grid(int d, long long tokens, int heads, int* gx, int* gy, int* heads_per);
+void norm_rope_bwd_grid(int d, long long tokens, int h, int h_kv, int* gx, int* gy, int* heads_per);
 cudaError_t launch_norm_rope(int d, const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(int d, const NormRopeParams& p, cudaStream_t stream);
 
@@ -288,7 +311,7 @@ struct CacheParams {
   __nv_bfloat16 *k_out, *v_out;    // read: [B, h_kv, m, d]
   const int* kv_len;               // [B] or nullptr (m)
   const int* new_len;              // [B] or nullptr (n)
-  long long rows;                  // write: B h_kv n; read: B h_kv m
+  unsigned long long rows;         // write: B h_kv n; read: B h_kv m; below 2^32
   int h_kv, n, m;
 };
 cudaError_t launch_cache_write(int d, bool quantised, const CacheParams& p, cudaStream_t stream);
@@ -310,7 +333,7 @@ struct TreeParams {
   const unsigned char *k_exp, *v_exp;  // [B h_kv][m] (e4m3 caches)
   int B, h_kv, n, rows, m;         // rows = (h / h_kv) n
   int row_blocks, block_rows;      // query rows of a key head in blocks of block_rows
-  int neg;                         // tensor-core kernel: scale < 0, and c = |scale| log2(e)
+  int by_unit;                     // a CTA for each unit (attn_tree.cuh)
   float c;                         // scale log2(e)
   Watchdog wd;
 };
@@ -320,6 +343,7 @@ struct TreePlan {
   bool tc;                 // the tcgen05 kernel (128-row query tiles), else mma.sync (16 rows)
   int tile;                // keys of a TMA box
   int row_blocks, block_rows;
+  bool by_unit;            // a CTA for each (sequence, key head, row block); no partial results
   int grid;                // CTAs
   long long slots;         // partial results
 };

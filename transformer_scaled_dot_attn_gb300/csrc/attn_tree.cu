@@ -33,6 +33,7 @@ constexpr int kTreeThreads = kTreeWarps * 32;
 constexpr int kTreeRows = 16;     // query rows of a CTA (one mma.sync tile)
 constexpr int kTreeLeast = 2;     // tiles (of four warps) worth a CTA of their own
 constexpr int kTreeLeastTc = 2;   // the same for the tcgen05 kernel
+constexpr int kTreeShort = 8;     // tiles of a cache that one CTA takes alone
 
 template <int D, bool Q8>
 struct Tree {
@@ -43,7 +44,7 @@ struct Tree {
   static constexpr uint32_t BOX = TK * ROWB;
   static constexpr int NBOX = D * ES / ROWB;
   static constexpr int BN = kTreeWarps * TK;               // keys of a CTA's tile
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = 2;
   static constexpr int CTAS = D == 128 ? 2 : 4;            // per SM
   static constexpr int NT = TK / 8;                        // n8 score tiles
   static constexpr int KS = D / 16;                        // k steps of the score product
@@ -79,10 +80,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
-}
-
-__device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t high_bytes) {
-  return mul_bf16x2(e4m3_places(high_bytes), 0x7b807b80u);  // 2^120, twice
 }
 
 __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
@@ -151,12 +148,12 @@ __device__ __forceinline__ void tree_drain(uint64_t* bar, uint32_t parity, const
   }
 }
 
+// A value of the tile, for the rare rows that add one that is not finite themselves.
 template <int D, bool Q8>
 __device__ __forceinline__ float value_at(const uint8_t* tile, int r, int c) {
   if constexpr (Q8) {
     const uint32_t code = tile[tile_off<D, true>(r, c)];
-    if ((code & 0x7fu) == 0x7fu) return __uint_as_float(0x7fc00000u);
-    return __uint_as_float(e4m3_to_bf16x2(code << 8) << 16);
+    return (code & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : 0.f;  // only NaN matters here
   } else {
     const uint16_t h = *reinterpret_cast<const uint16_t*>(tile + tile_off<D, false>(r, 2 * c));
     return __uint_as_float(static_cast<uint32_t>(h) << 16);
@@ -181,13 +178,48 @@ __device__ __forceinline__ uint32_t clean_pair(uint32_t v, bool lo_real, bool hi
   return v;
 }
 
+// The k steps of the score product for a key's words (e4m3): word k holds the
+// key's four codes that stand in columns 2t, 2t + 1, 2t + 8, 2t + 9 of step k.
+template <int D>
+__device__ __forceinline__ void key_words(const uint8_t* tile, int r, int t, uint32_t (&w)[D / 16]) {
+  if constexpr (D == 128) {
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + tile_off<D, true>(r, 16 * t));
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + tile_off<D, true>(r, 16 * (t + 4)));
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+  } else if constexpr (D == 64) {
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + tile_off<D, true>(r, 16 * t));
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(tile + tile_off<D, true>(r, 8 * t));
+    w[0] = u.x, w[1] = u.y;
+  }
+}
+
+// The D / 8 codes of position r in product column g's output columns.
+template <int D>
+__device__ __forceinline__ void value_words(const uint8_t* tile, int r, int g, uint32_t (&w)[D / 32]) {
+  const uint8_t* src = tile + tile_off<D, true>(r, col_of<D>(g) * (D / 8));
+  if constexpr (D == 128) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (D == 64) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(src);
+  }
+}
+
 // One CTA per share of the line of tiles (attn_tree.cuh); a tile is the four
-// warps' TK keys each.
-template <int D, bool Q8>
+// warps' TK keys each. HALF: at most 8 query rows, so that rows 8 to 15 of the
+// products are left out of the softmax.
+template <int D, bool Q8, bool HALF>
 __global__ void __launch_bounds__(kTreeThreads, Tree<D, Q8>::CTAS)
 attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const TreeParams p) {
   using C = Tree<D, Q8>;
+  constexpr int H = HALF ? 1 : 2;  // halves of the 16 rows in use: a thread's rows are g and g + 8
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kTreeWarps][C::STAGES];
   __shared__ int abort_word;
@@ -198,6 +230,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const int g = lane >> 2, t = lane & 3;
   volatile int* abort_flag = &abort_word;
   const Watchdog wd = p.wd;
+  grid_launch_dependents();
   TreeWalk walk;
   if (!tree_start(p, C::BN, kTreeLeast, walk)) return;
   if (tid == 0) {
@@ -214,353 +247,342 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   TreePart part;
 #pragma unroll 1
   while (tree_next(p, C::BN, walk, part)) {
-  const int bh = part.bh, b = part.b, row0 = part.rb * kTreeRows;
-  const int L = part.L;
-  const int old = L - p.n;  // positions before the newest n (negative: fewer cached than n)
-  const int mine = part.t1 - part.t0;  // of every tile this warp takes keys [warp TK, warp TK + TK)
-  const int key0 = part.t0 * C::BN + warp * C::TK;
-  auto load = [&](int x) {
-    const int st = (turn + x) % C::STAGES;
-    const int k0 = key0 + x * C::BN;
-    uint8_t* dst = ring + st * 2 * C::KT;
-    mbar_arrive_expect_tx(&full[warp][st], 2 * C::KT);
-    for (int a = 0; a < C::NBOX; ++a) {
-      tma_load_3d(dst + a * C::BOX, &tm_k, &full[warp][st], a * (C::ROWB / C::ES), k0, bh);
-      tma_load_3d(dst + C::KT + a * C::BOX, &tm_v, &full[warp][st], a * (C::ROWB / C::ES), k0, bh);
-    }
-  };
-  if (lane == 0)
-    for (int x = 0; x < C::STAGES && x < mine; ++x) load(x);
-
-  // the queries as the A operand: rows g and g + 8 of the block. e4m3 caches
-  // multiply in f16, which holds every code; the query row is brought to
-  // [2^14, 2^15) by a power of two first, so that what f16 cannot hold of it
-  // lies 2^-39 below its largest element.
-  const int r0 = row0 + g, r1 = r0 + 8;
-  const __nv_bfloat16* qrow0 = p.q + (static_cast<size_t>(bh) * p.rows + min(r0, p.rows - 1)) * D;
-  const __nv_bfloat16* qrow1 = p.q + (static_cast<size_t>(bh) * p.rows + min(r1, p.rows - 1)) * D;
-  uint32_t qa[C::KS][4];
-  float c0 = p.c, c1 = p.c;  // per row: scale log2(e), and for e4m3 the inverse of the query's power of two
-  if constexpr (Q8) {
-    uint32_t a0 = 0, a1 = 0;
-#pragma unroll
-    for (int s = 0; s < C::KS; ++s) {
-      const int at = D == 128 ? 16 * (t + 4 * (s >> 2)) + 4 * (s & 3) : D == 64 ? 16 * t + 4 * s : 8 * t + 4 * s;
-      const uint2 u = *reinterpret_cast<const uint2*>(qrow0 + at);
-      const uint2 v = *reinterpret_cast<const uint2*>(qrow1 + at);
-      qa[s][0] = u.x;
-      qa[s][1] = v.x;
-      qa[s][2] = u.y;
-      qa[s][3] = v.y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = qa[s][e] & 0x7fffu, hi = (qa[s][e] >> 16) & 0x7fffu;
-        uint32_t& a = (e & 1) ? a1 : a0;
-        a = max(a, lo < 0x7f80u ? lo : 0u);
-        a = max(a, hi < 0x7f80u ? hi : 0u);
+    const int bh = part.bh, row0 = part.rb * kTreeRows, L = part.L;
+    const int old = L - p.n;             // positions before the newest n (negative: fewer cached than n)
+    const int mine = part.t1 - part.t0;  // of every tile this warp takes keys [warp TK, warp TK + TK)
+    const int key0 = part.t0 * C::BN + warp * C::TK;
+    auto load = [&](int x) {
+      const int st = (turn + x) % C::STAGES;
+      const int k0 = key0 + x * C::BN;
+      uint8_t* dst = ring + st * 2 * C::KT;
+      mbar_arrive_expect_tx(&full[warp][st], 2 * C::KT);
+      for (int a = 0; a < C::NBOX; ++a) {
+        tma_load_3d(dst + a * C::BOX, &tm_k, &full[warp][st], a * (C::ROWB / C::ES), k0, bh);
+        tma_load_3d(dst + C::KT + a * C::BOX, &tm_v, &full[warp][st], a * (C::ROWB / C::ES), k0, bh);
       }
-    }
+    };
+    if (lane == 0)
+      for (int x = 0; x < C::STAGES && x < mine; ++x) load(x);
+
+    // The queries as the A operand (negated for a negative scale, so that the
+    // factor below is positive). e4m3 caches multiply in f16, which holds every
+    // code; the query row is brought to [2^14, 2^15) by a power of two first, so
+    // that what f16 cannot hold of it lies 2^-39 below its largest element.
+    uint32_t qa[C::KS][4];
+    float c[H];  // per row: |scale| log2(e), and for e4m3 the inverse of the row's power of two
+    unsigned long long word[H];
 #pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-      a0 = max(a0, __shfl_xor_sync(0xffffffffu, a0, o));
-      a1 = max(a1, __shfl_xor_sync(0xffffffffu, a1, o));
-    }
-    const uint32_t e0 = 268u - max(a0 >> 7, 15u), e1 = 268u - max(a1 >> 7, 15u);
-    const float u0 = __uint_as_float(e0 << 23), u1 = __uint_as_float(e1 << 23);
-    c0 *= __uint_as_float((254u - e0) << 23);
-    c1 *= __uint_as_float((254u - e1) << 23);
+    for (int h = 0; h < 2; ++h) {
+      if (h >= H) {
 #pragma unroll
-    for (int s = 0; s < C::KS; ++s)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = unpack_bf16x2(qa[s][e]);
-        const float f = (e & 1) ? u1 : u0;
-        qa[s][e] = pack_f16x2(x.x * f, x.y * f);
+        for (int s = 0; s < C::KS; ++s) qa[s][1] = qa[s][3] = 0u;
+        break;
       }
-  } else {
-#pragma unroll
-    for (int s = 0; s < C::KS; ++s) {
-      qa[s][0] = *reinterpret_cast<const uint32_t*>(qrow0 + 16 * s + 2 * t);
-      qa[s][1] = *reinterpret_cast<const uint32_t*>(qrow1 + 16 * s + 2 * t);
-      qa[s][2] = *reinterpret_cast<const uint32_t*>(qrow0 + 16 * s + 8 + 2 * t);
-      qa[s][3] = *reinterpret_cast<const uint32_t*>(qrow1 + 16 * s + 8 + 2 * t);
-    }
-  }
-  const unsigned long long word0 = tree_word(p, b, min(r0, p.rows - 1));
-  const unsigned long long word1 = tree_word(p, b, min(r1, p.rows - 1));
-  // keys of score columns 2t and 2t + 1 within a group of eight
-  const int ka = Q8 ? key_of<D>(2 * t) : 2 * t, kb = Q8 ? key_of<D>(2 * t + 1) : 2 * t + 1;
-
-  float acc[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this thread's columns only
-
-  // e4m3: lane j holds the scale bytes of key j of the tile, read one tile ahead
-  int ke = 127, ve = 127;
-  auto scales = [&](int x) {
-    const int key = key0 + x * C::BN + lane;
-    const bool in = x < mine && key < L;
-    const size_t at = static_cast<size_t>(bh) * p.m + key;
-    ke = in ? __ldg(p.k_exp + at) : 127;
-    ve = in ? __ldg(p.v_exp + at) : 127;
-  };
-  if constexpr (Q8) scales(0);
-
-  int x = 0;
-  for (; x < mine; ++x) {
-    const int st = (turn + x) % C::STAGES;
-    const int k0 = key0 + x * C::BN;
-    const uint8_t* sk = ring + st * 2 * C::KT;
-    const uint8_t* sv = sk + C::KT;
-    const uint32_t ak = smem_u32(sk), av = smem_u32(sv);
-    const int my_ke = ke, my_ve = ve;
-    if constexpr (Q8) scales(x + 1);
-    if (!__all_sync(0xffffffffu, tree_wait(&full[warp][st], ((turn + x) / C::STAGES) & 1, abort_flag, wd))) break;
-
-    // scores of the tile's keys
-    float s[C::NT][4];
-#pragma unroll
-    for (int i = 0; i < C::NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-    if constexpr (Q8) {
-#pragma unroll
-      for (int i = 0; i < C::NT; ++i) {
-        const int r = i * 8 + key_of<D>(g);
-        uint32_t w[D / 16];
-        if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sk + tile_off<D, true>(r, 16 * t));
-          const uint4 v = *reinterpret_cast<const uint4*>(sk + tile_off<D, true>(r, 16 * (t + 4)));
-          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-          w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
-        } else if constexpr (D == 64) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sk + tile_off<D, true>(r, 16 * t));
-          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(sk + tile_off<D, true>(r, 8 * t));
-          w[0] = u.x, w[1] = u.y;
-        }
-#pragma unroll
-        for (int k = 0; k < C::KS; ++k)
-          mma_f16(s[i], qa[k], e4m3_to_f16x2(w[k] & 0xffffu), e4m3_to_f16x2(w[k] >> 16));
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < C::KS; k += 2)
-#pragma unroll
-        for (int i = 0; i < C::NT; ++i) {
-          uint32_t w[4];
-          ldsm4(ak + tile_off<D, false>(i * 8 + (lane & 7), (2 * k + (lane >> 3)) * 16), w);
-          mma_bf16(s[i], qa[k], w[0], w[1]);
-          mma_bf16(s[i], qa[k + 1], w[2], w[3]);
-        }
-    }
-    // in units of log2, masked where the tile reaches past the positions that every row sees
-    const bool tail = k0 + C::TK > old;
-    float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < C::NT; ++i) {
-      float fa = 1.f, fb = 1.f;
+      const int row = min(row0 + g + 8 * h, p.rows - 1);
+      const __nv_bfloat16* q = p.q + (static_cast<size_t>(bh) * p.rows + row) * D;
+      const uint32_t sign = p.c < 0.f ? 0x80008000u : 0u;
+      word[h] = tree_word(p, part.b, row);
+      c[h] = fmaxf(fabsf(p.c), 1e-30f);  // (scale 0: 0 times the -inf of a masked score would be NaN)
       if constexpr (Q8) {
-        fa = pow2_of_byte(__shfl_sync(0xffffffffu, my_ke, i * 8 + ka));
-        fb = pow2_of_byte(__shfl_sync(0xffffffffu, my_ke, i * 8 + kb));
-      }
-      s[i][0] *= c0 * fa;
-      s[i][1] *= c0 * fb;
-      s[i][2] *= c1 * fa;
-      s[i][3] *= c1 * fb;
-      if (tail) {
-        const int ja = k0 + i * 8 + ka, jb = k0 + i * 8 + kb;
-        if (!sees(word0, ja, old, L)) s[i][0] = -INFINITY;
-        if (!sees(word0, jb, old, L)) s[i][1] = -INFINITY;
-        if (!sees(word1, ja, old, L)) s[i][2] = -INFINITY;
-        if (!sees(word1, jb, old, L)) s[i][3] = -INFINITY;
-      }
-      t0 = fmaxf(t0, fmaxf(s[i][0], s[i][1]));
-      t1 = fmaxf(t1, fmaxf(s[i][2], s[i][3]));
-    }
+        uint32_t top = 0;
 #pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, o));
-      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, o));
-    }
-    if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
-      const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
-      const float a0 = ex2_approx(m0 - (n0 == -INFINITY ? 0.f : n0)), a1 = ex2_approx(m1 - (n1 == -INFINITY ? 0.f : n1));
-      m0 = n0;
-      m1 = n1;
-      l0 *= a0;
-      l1 *= a1;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        acc[i][0] *= a0;
-        acc[i][1] *= a0;
-        acc[i][2] *= a1;
-        acc[i][3] *= a1;
-      }
-    }
-    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;  // nothing seen yet: weights 0
-
-    // weights (bf16; the e4m3 row's scale goes into them) and P V, 16 keys at a time
-    bool odd = false;
-    uint32_t nans = 0;
-#pragma unroll
-    for (int kk = 0; kk < C::TK / 16; ++kk) {
-      uint32_t pa[4];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float* si = s[2 * kk + u];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) si[e] = ex2_approx(si[e] - (e < 2 ? b0 : b1));
-        l0 += si[0] + si[1];
-        l1 += si[2] + si[3];
-        if constexpr (Q8) {
-          const float fa = pow2_of_byte(__shfl_sync(0xffffffffu, my_ve, (2 * kk + u) * 8 + ka));
-          const float fb = pow2_of_byte(__shfl_sync(0xffffffffu, my_ve, (2 * kk + u) * 8 + kb));
-          si[0] *= fa;
-          si[1] *= fb;
-          si[2] *= fa;
-          si[3] *= fb;
-        }
-        pa[2 * u] = pack_bf16x2(si[0], si[1]);
-        pa[2 * u + 1] = pack_bf16x2(si[2], si[3]);
-      }
-      if constexpr (Q8) {
-        constexpr int W = D / 32;  // words of this thread's columns in a row
-        uint32_t w[4][W];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = kk * 16 + (u >> 1) * 8 + ((u & 1) ? kb : ka);
-          const uint8_t* src = sv + tile_off<D, true>(r, col_of<D>(g) * (D / 8));
-          if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src);
-            w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
-          } else if constexpr (D == 64) {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            w[u][0] = v.x, w[u][1] = v.y;
-          } else {
-            w[u][0] = *reinterpret_cast<const uint32_t*>(src);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          nans |= nan_codes(w[0][i]) | nan_codes(w[1][i]) | nan_codes(w[2][i]) | nan_codes(w[3][i]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // byte e of both keys' words, each in the high byte of a half
-            // (what stands in the low bytes is masked away)
-            const uint32_t pick = (e << 4) | ((4u + e) << 12);
-            const uint32_t v0 = e4m3_to_bf16x2(__byte_perm(w[0][i], w[1][i], pick));
-            const uint32_t v1 = e4m3_to_bf16x2(__byte_perm(w[2][i], w[3][i], pick));
-            mma_bf16(acc[4 * i + e], pa, v0, v1);
-          }
-        }
-      } else {
-        const int base = k0 + kk * 16;
-        const bool ra = base + ka < L, rb = base + kb < L, rc = base + 8 + ka < L, rd = base + 8 + kb < L;
-#pragma unroll
-        for (int i = 0; i < D / 8; i += 2) {
-          uint32_t v[4];
-          ldsm4_t(av + tile_off<D, false>(kk * 16 + (lane & 15), (i + (lane >> 4)) * 16), v);
-          if (tail) {
-            v[0] = clean_pair(v[0], ra, rb, odd);
-            v[1] = clean_pair(v[1], rc, rd, odd);
-            v[2] = clean_pair(v[2], ra, rb, odd);
-            v[3] = clean_pair(v[3], rc, rd, odd);
-          }
-          mma_bf16(acc[i], pa, v[0], v[1]);
-          mma_bf16(acc[i + 1], pa, v[2], v[3]);
-        }
-      }
-    }
-    if (__any_sync(0xffffffffu, odd || (nans & 0x80808080u) != 0)) {
-      // values left out above that are not finite (bf16: of a tile that some row
-      // sees in part; e4m3: any): only for the rows that see them
-#pragma unroll 1
-      for (int j = 0; j < C::TK; ++j) {
-        const bool v0 = sees(word0, k0 + j, old, L), v1 = sees(word1, k0 + j, old, L);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int s = 0; s < C::KS; ++s) {
+          const int at = D == 128 ? 16 * (t + 4 * (s >> 2)) + 4 * (s & 3) : D == 64 ? 16 * t + 4 * s : 8 * t + 4 * s;
+          const uint2 u = *reinterpret_cast<const uint2*>(q + at);
+          qa[s][h] = u.x ^ sign;
+          qa[s][2 + h] = u.y ^ sign;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int col = Q8 ? col_of<D>(2 * t + e) * (D / 8) + i : i * 8 + 2 * t + e;
-            const float v = value_at<D, Q8>(sv, j, col);
-            const bool off = (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u;
-            if (off && v0) acc[i][e] += v;
-            if (off && v1) acc[i][2 + e] += v;
+            const uint32_t w = qa[s][2 * e + h], lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+            top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+          }
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t up = 268u - max(top >> 7, 15u);
+        const float f = __uint_as_float(up << 23);
+        c[h] = fmaxf(c[h] * __uint_as_float((254u - up) << 23), 1e-37f);
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = unpack_bf16x2(qa[s][2 * e + h]);
+            qa[s][2 * e + h] = pack_f16x2(x.x * f, x.y * f);
+          }
+      } else {
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s) {
+          qa[s][h] = *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t) ^ sign;
+          qa[s][2 + h] = *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * t) ^ sign;
+        }
+      }
+    }
+    // keys of score columns 2t and 2t + 1 within a group of eight
+    const int ka = Q8 ? key_of<D>(2 * t) : 2 * t, kb = Q8 ? key_of<D>(2 * t + 1) : 2 * t + 1;
+
+    float acc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    float m[H], l[H];  // l: this thread's columns only
+#pragma unroll
+    for (int h = 0; h < H; ++h) m[h] = -INFINITY, l[h] = 0.f;
+
+    // e4m3: lane j holds the scale bytes of key j of the tile, read one tile
+    // ahead. V's scales go into the weights, relative to the largest met so far
+    // (`top_v`), so that the weights fit f16: p 2^(e - top_v) 2^15.
+    int ke = 0, ve = 0, top_v = 0;
+    auto scales = [&](int x) {
+      const int key = key0 + x * C::BN + lane;
+      const bool in = x < mine && key < L;
+      const size_t at = static_cast<size_t>(bh) * p.m + key;
+      ke = in ? __ldg(p.k_exp + at) : 0;
+      ve = in ? __ldg(p.v_exp + at) : 0;
+    };
+    if constexpr (Q8) scales(0);
+
+    int x = 0;
+    for (; x < mine; ++x) {
+      const int st = (turn + x) % C::STAGES;
+      const int k0 = key0 + x * C::BN;
+      const uint8_t* sk = ring + st * 2 * C::KT;
+      const uint8_t* sv = sk + C::KT;
+      const uint32_t ak = smem_u32(sk), av = smem_u32(sv);
+      float fk = 1.f, fv = 1.f, back = 1.f;
+      if constexpr (Q8) {
+        fk = pow2_of_byte(ke);
+        const int top = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(ve)));
+        if (top > top_v) {
+          back = ex2_approx(static_cast<float>(top_v - top));  // (an empty product before the first: any factor)
+          top_v = top;
+        }
+        const int e = ve - top_v + 127 + 15;
+        fv = e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.f;
+        scales(x + 1);
+      }
+      if (!__all_sync(0xffffffffu, tree_wait(&full[warp][st], ((turn + x) / C::STAGES) & 1, abort_flag, wd))) break;
+
+      // scores of the tile's keys
+      float s[C::NT][4];
+#pragma unroll
+      for (int i = 0; i < C::NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      if constexpr (Q8) {
+#pragma unroll
+        for (int i = 0; i < C::NT; ++i) {
+          uint32_t w[C::KS];
+          key_words<D>(sk, i * 8 + key_of<D>(g), t, w);
+#pragma unroll
+          for (int k = 0; k < C::KS; ++k)
+            mma_f16(s[i], qa[k], e4m3_to_f16x2(w[k] & 0xffffu), e4m3_to_f16x2(w[k] >> 16));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < C::KS; k += 2)
+#pragma unroll
+          for (int i = 0; i < C::NT; ++i) {
+            uint32_t w[4];
+            ldsm4(ak + tile_off<D, false>(i * 8 + (lane & 7), (2 * k + (lane >> 3)) * 16), w);
+            mma_bf16(s[i], qa[k], w[0], w[1]);
+            mma_bf16(s[i], qa[k + 1], w[2], w[3]);
           }
       }
-    }
-    __syncwarp();
-    if (lane == 0 && x + C::STAGES < mine) {
-      fence_proxy_async_smem();  // the warp's reads of the stage come before the TMA write
-      load(x + C::STAGES);
-    }
-  }
-  if (x < mine && lane == 0)  // the watchdog fired: let the tiles in flight land
-    for (int y = x; y < x + C::STAGES && y < mine; ++y)
-      tree_drain(&full[warp][(turn + y) % C::STAGES], ((turn + y) / C::STAGES) & 1, wd);
-  // join the four warps' results; every load has landed
+      // the keys' scales, and the mask where the tile reaches past the positions that every row sees
+      const bool tail = k0 + C::TK > old;
+      float top[H];
 #pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-  }
-  // (a row whose every score was NaN has no maximum: its sum is NaN, against the reference 0)
-  if (m0 == -INFINITY && l0 != 0.f) m0 = 0.f;
-  if (m1 == -INFINITY && l1 != 0.f) m1 = 0.f;
-  if (__syncthreads_or(x < mine)) return;
-  float* so = reinterpret_cast<float*>(smem) + warp * (kTreeRows * C::OST);
+      for (int h = 0; h < H; ++h) top[h] = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < C::NT; ++i) {
+        if constexpr (Q8) {
+          const float fa = __shfl_sync(0xffffffffu, fk, i * 8 + ka), fb = __shfl_sync(0xffffffffu, fk, i * 8 + kb);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int col = Q8 ? col_of<D>(2 * t + e) * (D / 8) + i : i * 8 + 2 * t + e;
-      so[g * C::OST + col] = acc[i][e];
-      so[(g + 8) * C::OST + col] = acc[i][2 + e];
-    }
-  if (t == 0) {
-    s_m[warp][g] = m0;
-    s_m[warp][g + 8] = m1;
-    s_l[warp][g] = l0;
-    s_l[warp][g + 8] = l1;
-  }
-  __syncthreads();
-  const float* sall = reinterpret_cast<const float*>(smem);
-  constexpr int TPR = kTreeThreads / kTreeRows;  // threads of an output row
-  const int r = tid / TPR, row = row0 + r;
-  float M = -INFINITY, l = 0.f, f[kTreeWarps];
+          for (int h = 0; h < H; ++h) s[i][2 * h] *= fa, s[i][2 * h + 1] *= fb;
+        }
+        if (tail) {
+          const int ja = k0 + i * 8 + ka, jb = k0 + i * 8 + kb;
 #pragma unroll
-  for (int w = 0; w < kTreeWarps; ++w) M = fmaxf(M, s_m[w][r]);
+          for (int h = 0; h < H; ++h) {
+            if (!sees(word[h], ja, old, L)) s[i][2 * h] = -INFINITY;
+            if (!sees(word[h], jb, old, L)) s[i][2 * h + 1] = -INFINITY;
+          }
+        }
 #pragma unroll
-  for (int w = 0; w < kTreeWarps; ++w) {
-    f[w] = M == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - M);
-    l = fmaf(f[w], s_l[w][r], l);
-  }
-  auto sum_of = [&](int c) {
-    float o = 0.f;
-#pragma unroll
-    for (int w = 0; w < kTreeWarps; ++w) o = fmaf(f[w], sall[(w * kTreeRows + r) * C::OST + c], o);
-    return o;
-  };
-  if (row < p.rows) {
-    const float inv = M == -INFINITY ? 0.f : 1.f / l;  // a row that saw no key is the empty sum
-    if (part.whole) {
-      const size_t out = static_cast<size_t>(bh) * p.rows + row;
-      for (int c = (tid % TPR) * 2; c < D; c += TPR * 2) {
-        const uint32_t v = pack_bf16x2(sum_of(c) * inv, sum_of(c + 1) * inv);
-        *reinterpret_cast<uint32_t*>(p.o + out * D + c) = v;
+        for (int h = 0; h < H; ++h) top[h] = fmaxf(top[h], fmaxf(s[i][2 * h], s[i][2 * h + 1]));
       }
-      if (tid % TPR == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * kTreeLn2;
-    } else {
-      const size_t at = static_cast<size_t>(part.slot) * p.block_rows + r;
-      for (int c = (tid % TPR) * 2; c < D; c += TPR * 2)
-        *reinterpret_cast<float2*>(p.part + at * D + c) = make_float2(sum_of(c), sum_of(c + 1));
-      if (tid % TPR == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(M, l);
+      bool grew = Q8 && back != 1.f;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2)) * c[h];  // in units of log2
+        grew |= top[h] > m[h];
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const float n = fmaxf(m[h], top[h]);
+          const float f = ex2_approx(m[h] - (n == -INFINITY ? 0.f : n));
+          m[h] = n;
+          l[h] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            acc[i][2 * h] *= f * back;
+            acc[i][2 * h + 1] *= f * back;
+          }
+        }
+      }
+      float ref[H];  // nothing seen yet: weights 0
+#pragma unroll
+      for (int h = 0; h < H; ++h) ref[h] = m[h] == -INFINITY ? 0.f : m[h];
+
+      // weights and P V, 16 keys at a time. The weights are rounded to the
+      // caches' product type: bf16 (2^-9 of a weight), f16 for e4m3 (2^-12).
+      bool odd = false;
+#pragma unroll
+      for (int kk = 0; kk < C::TK / 16; ++kk) {
+        uint32_t pa[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float* si = s[2 * kk + u];
+          float fa = 1.f, fb = 1.f;
+          if constexpr (Q8) {
+            fa = __shfl_sync(0xffffffffu, fv, (2 * kk + u) * 8 + ka);
+            fb = __shfl_sync(0xffffffffu, fv, (2 * kk + u) * 8 + kb);
+          }
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            const float w0 = ex2_approx(fmaf(si[2 * h], c[h], -ref[h]));
+            const float w1 = ex2_approx(fmaf(si[2 * h + 1], c[h], -ref[h]));
+            l[h] += w0 + w1;
+            pa[2 * u + h] = Q8 ? pack_f16x2(w0 * fa, w1 * fb) : pack_bf16x2(w0, w1);
+          }
+        }
+        if constexpr (Q8) {
+          constexpr int W = D / 32;  // words of this thread's columns in a row
+          uint32_t w[4][W];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            value_words<D>(sv, kk * 16 + (u >> 1) * 8 + ((u & 1) ? kb : ka), g, w[u]);
+          if (tail) {
+            // NaN codes may not enter a product here: a weight of 0 would make
+            // them NaN for rows that do not see them
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int i = 0; i < W; ++i) {
+                const uint32_t n = nan_codes(w[u][i]) & 0x80808080u;
+                if (n != 0) {
+                  odd = true;
+                  w[u][i] &= ~((n >> 7) * 0xffu);
+                }
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            // codes of the keys of columns 2t, 2t + 1 side by side, then of 2t + 8, 2t + 9
+            const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5140), a1 = __byte_perm(w[0][i], w[1][i], 0x7362);
+            const uint32_t b0 = __byte_perm(w[2][i], w[3][i], 0x5140), b1 = __byte_perm(w[2][i], w[3][i], 0x7362);
+            mma_f16(acc[4 * i], pa, e4m3_to_f16x2(a0 & 0xffffu), e4m3_to_f16x2(b0 & 0xffffu));
+            mma_f16(acc[4 * i + 1], pa, e4m3_to_f16x2(a0 >> 16), e4m3_to_f16x2(b0 >> 16));
+            mma_f16(acc[4 * i + 2], pa, e4m3_to_f16x2(a1 & 0xffffu), e4m3_to_f16x2(b1 & 0xffffu));
+            mma_f16(acc[4 * i + 3], pa, e4m3_to_f16x2(a1 >> 16), e4m3_to_f16x2(b1 >> 16));
+          }
+        } else {
+          const int base = k0 + kk * 16;
+          const bool ra = base + ka < L, rb = base + kb < L, rc = base + 8 + ka < L, rd = base + 8 + kb < L;
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 2) {
+            uint32_t v[4];
+            ldsm4_t(av + tile_off<D, false>(kk * 16 + (lane & 15), (i + (lane >> 4)) * 16), v);
+            if (tail) {
+              v[0] = clean_pair(v[0], ra, rb, odd);
+              v[1] = clean_pair(v[1], rc, rd, odd);
+              v[2] = clean_pair(v[2], ra, rb, odd);
+              v[3] = clean_pair(v[3], rc, rd, odd);
+            }
+            mma_bf16(acc[i], pa, v[0], v[1]);
+            mma_bf16(acc[i + 1], pa, v[2], v[3]);
+          }
+        }
+      }
+      if (tail && __any_sync(0xffffffffu, odd)) {
+        // values left out above that are not finite: only for the rows that see them
+#pragma unroll 1
+        for (int j = 0; j < C::TK; ++j)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (sees(word[h], k0 + j, old, L))
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float v = value_at<D, Q8>(sv, j, Q8 ? col_of<D>(2 * t + e) * (D / 8) + i : i * 8 + 2 * t + e);
+                  if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) acc[i][2 * h + e] += v;
+                }
+      }
+      __syncwarp();
+      if (lane == 0 && x + C::STAGES < mine) {
+        fence_proxy_async_smem();  // the warp's reads of the stage come before the TMA write
+        load(x + C::STAGES);
+      }
     }
-  }
-  turn += mine;
-  fence_proxy_async_smem();  // the results in the ring come before the next part's TMA writes
-  __syncthreads();
+    if (x < mine && lane == 0)  // the watchdog fired: let the tiles in flight land
+      for (int y = x; y < x + C::STAGES && y < mine; ++y)
+        tree_drain(&full[warp][(turn + y) % C::STAGES], ((turn + y) / C::STAGES) & 1, wd);
+    // join the four warps' results; every load has landed
+    if (__syncthreads_or(x < mine)) return;
+    float* so = reinterpret_cast<float*>(smem) + warp * (kTreeRows * C::OST);
+    const float unit_v = Q8 ? pow2_of_byte(top_v) * 0x1p-15f : 1.f;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      // a row whose every score was NaN has no maximum: its sum is NaN, against the reference 0
+      if (m[h] == -INFINITY && l[h] != 0.f) m[h] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          so[(g + 8 * h) * C::OST + (Q8 ? col_of<D>(2 * t + e) * (D / 8) + i : i * 8 + 2 * t + e)] =
+              acc[i][2 * h + e] * unit_v;
+      if (t == 0) {
+        s_m[warp][g + 8 * h] = m[h];
+        s_l[warp][g + 8 * h] = l[h];
+      }
+    }
+    __syncthreads();
+    const float* sall = reinterpret_cast<const float*>(smem);
+    constexpr int TPR = kTreeThreads / (8 * H);  // threads of an output row
+    const int r = tid / TPR, row = row0 + r;
+    if (row < p.rows) {
+      float M = -INFINITY, sum = 0.f, f[kTreeWarps];
+#pragma unroll
+      for (int w = 0; w < kTreeWarps; ++w) M = fmaxf(M, s_m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kTreeWarps; ++w) {
+        f[w] = M == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - M);
+        sum = fmaf(f[w], s_l[w][r], sum);
+      }
+      auto joined = [&](int col) {
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kTreeWarps; ++w) o = fmaf(f[w], sall[(w * kTreeRows + r) * C::OST + col], o);
+        return o;
+      };
+      if (part.whole) {
+        const float inv = M == -INFINITY ? 0.f : 1.f / sum;  // a row that saw no key is the empty sum
+        const size_t out = static_cast<size_t>(bh) * p.rows + row;
+        for (int col = (tid % TPR) * 2; col < D; col += TPR * 2)
+          *reinterpret_cast<uint32_t*>(p.o + out * D + col) = pack_bf16x2(joined(col) * inv, joined(col + 1) * inv);
+        if (tid % TPR == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
+      } else {
+        const size_t at = static_cast<size_t>(part.slot) * p.block_rows + r;
+        for (int col = (tid % TPR) * 2; col < D; col += TPR * 2)
+          *reinterpret_cast<float2*>(p.part + at * D + col) = make_float2(joined(col), joined(col + 1));
+        if (tid % TPR == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(M, sum);
+      }
+    }
+    turn += mine;
+    fence_proxy_async_smem();  // the results in the ring come before the next part's TMA writes
+    __syncthreads();
   }
 }
 
@@ -569,6 +591,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 template <int D>
 __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p, int bn, int grid, int least) {
   const TreeLine l = tree_line(p, bn, grid, least);
+  grid_wait();  // the parts are written
   const int unit = blockIdx.x, lane = threadIdx.x & 31;
   const int b = unit / l.per_seq, idx = unit - b * l.per_seq;
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
@@ -630,7 +653,7 @@ bool tree_uses_tc(int rows, int d, bool quantised) {
   return rows > 32;
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool HALF>
 cudaError_t launch_small(int grid, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                          cudaStream_t stream) {
   using C = Tree<D, Q8>;
@@ -639,16 +662,23 @@ cudaError_t launch_small(int grid, const CUtensorMap& tk, const CUtensorMap& tv,
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!set[dev & 63].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(attn_tree_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_tree_kernel<D, Q8, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
     set[dev & 63].store(true, std::memory_order_relaxed);
   }
   prof_begin(kKindTree, stream);
-  attn_tree_kernel<D, Q8><<<static_cast<unsigned>(grid), kTreeThreads, C::SMEM, stream>>>(tk, tv, p);
+  attn_tree_kernel<D, Q8, HALF><<<static_cast<unsigned>(grid), kTreeThreads, C::SMEM, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   prof_end(kKindTree, stream);
   return e;
+}
+
+template <int D, bool Q8>
+cudaError_t launch_small_rows(int grid, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                              cudaStream_t stream) {
+  return p.block_rows <= 8 ? launch_small<D, Q8, true>(grid, tk, tv, p, stream)
+                           : launch_small<D, Q8, false>(grid, tk, tv, p, stream);
 }
 
 template <int D>
@@ -656,15 +686,15 @@ cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMa
                           const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   cudaError_t e;
   if (plan.tc) e = launch_tree_tc(D, quantised, plan.grid, kTreeLeastTc, tq, tk, tv, p, stream);
-  else if (quantised) e = launch_small<D, true>(plan.grid, tk, tv, p, stream);
-  else e = launch_small<D, false>(plan.grid, tk, tv, p, stream);
-  if (e != cudaSuccess || plan.grid == 1) return e;
+  else if (quantised) e = launch_small_rows<D, true>(plan.grid, tk, tv, p, stream);
+  else e = launch_small_rows<D, false>(plan.grid, tk, tv, p, stream);
+  if (e != cudaSuccess || plan.by_unit) return e;
   const unsigned units = static_cast<unsigned>(p.B) * p.h_kv * p.row_blocks;
   const int warps = p.block_rows < 8 ? p.block_rows : 8;
   prof_begin(kKindTreeMerge, stream);
-  attn_tree_merge_kernel<D><<<dim3(units, static_cast<unsigned>((p.block_rows + 7) / 8)), warps * 32, 0, stream>>>(
-      p, plan.tile, plan.grid, plan.tc ? kTreeLeastTc : kTreeLeast);
-  e = cudaGetLastError();
+  e = launch_dependent(attn_tree_merge_kernel<D>, dim3(units, static_cast<unsigned>((p.block_rows + 7) / 8)),
+                       dim3(static_cast<unsigned>(warps * 32)), stream, p, plan.tile, plan.grid,
+                       plan.tc ? kTreeLeastTc : kTreeLeast);
   prof_end(kKindTreeMerge, stream);
   return e;
 }
@@ -683,12 +713,19 @@ TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised) {
   }
   l.row_blocks = (rows + l.block_rows - 1) / l.block_rows;
   const long long units = static_cast<long long>(B) * h_kv * l.row_blocks;
-  // one CTA for each place on the GPU's SMs; fewer where the caches (at their
-  // capacity) hold too few tiles
-  const int least = l.tc ? kTreeLeastTc : kTreeLeast;
-  const long long most = (units * ((m + l.tile - 1) / l.tile) + least - 1) / least;
+  const long long tiles = (m + l.tile - 1) / l.tile;
   const long long room = static_cast<long long>(kSms) * (l.tc ? 1 : small_ctas(d, quantised));
-  l.grid = static_cast<int>(most < room ? most : room);
+  // Short caches: a CTA for each unit, nothing to join. Else one CTA for each
+  // place on the GPU's SMs; fewer where the caches hold too few tiles.
+  l.by_unit = tiles <= kTreeShort && (units <= room || (!l.tc && units <= 0x7fffffffLL));
+  if (l.by_unit) {
+    l.grid = static_cast<int>(units);
+  } else {
+    const int least = l.tc ? kTreeLeastTc : kTreeLeast;
+    const long long most = (units * tiles + least - 1) / least;
+    l.grid = static_cast<int>(most < room ? most : room);
+    if (l.grid == 1) l.by_unit = true;  // one tile of one unit
+  }
   l.slots = units + l.grid;
   return l;
 }

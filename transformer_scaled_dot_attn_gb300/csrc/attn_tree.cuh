@@ -86,6 +86,10 @@ __device__ __forceinline__ TreeLine tree_line(const TreeParams& p, int bn, int g
   return l;
 }
 
+__device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
+  return p.kv_len == nullptr ? p.m : min(max(__ldg(p.kv_len + b), 0), p.m);
+}
+
 // A CTA's position on the line: the sequence and unit it is at.
 struct TreeWalk {
   long long pos, end;   // tiles left: [pos, end)
@@ -103,12 +107,19 @@ struct TreePart {
   long long unit, slot;
 };
 
-__device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
-  return p.kv_len == nullptr ? p.m : min(max(__ldg(p.kv_len + b), 0), p.m);
-}
-
 // Every lane of a warp calls this; false: the CTA has no share.
 __device__ __forceinline__ bool tree_start(const TreeParams& p, int bn, int least, TreeWalk& w) {
+  if (p.by_unit) {  // short caches: CTA c takes unit c whole
+    const int per_seq = p.h_kv * p.row_blocks;
+    w.cta = 0;
+    w.b = static_cast<int>(blockIdx.x) / per_seq;
+    w.idx = static_cast<int>(blockIdx.x) - w.b * per_seq;
+    w.L = tree_len(p, w.b);
+    w.tiles = tiles_of(w.L, bn);
+    w.first = w.pos = 0;
+    w.end = w.tiles;
+    return true;
+  }
   const TreeLine l = tree_line(p, bn, static_cast<int>(gridDim.x), least);
   w.cta = static_cast<int>(blockIdx.x);
   if (w.cta >= l.ctas) return false;

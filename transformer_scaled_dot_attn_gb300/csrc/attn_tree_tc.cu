@@ -150,6 +150,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &sh.abort_flag;
   const Watchdog wd = p.wd;
+  grid_launch_dependents();
   TreeWalk walk;
   if (!tree_start(p, kBN, least, walk)) return;
   if (tid == 0) {
@@ -476,7 +477,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       // ---------------------------------------------------------- issuer of query tile g
       const int g = warp - C::ISSUER;
       if (lane == 0) {
-        const uint32_t idesc_s = idesc_bf16_f32(128, kBN, false, false) | (p.neg ? (1u << 13) : 0u);
+        const uint32_t idesc_s = idesc_bf16_f32(128, kBN, false, false) | (p.c < 0.f ? (1u << 13) : 0u);
         const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
         const uint32_t sq = smem_u32(smem + C::OFF_Q) + g * C::TILE;
         const uint32_t sb = smem_u32(smem + C::OFF_B);

@@ -88,12 +88,6 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // e4m3 caches: which key of a group of eight stands in column g of a product.
 // The order is chosen so that the threads that read shared memory together
 // meet every bank once, for K (rows of neighbouring g) and V (rows of one t).

@@ -12,17 +12,9 @@ __device__ __forceinline__ float pow2_of_byte(int byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : static_cast<uint32_t>(byte) << 23);
 }
 
-// Two e4m3 codes (the halves' high bytes) as a bf16 pair times 2^-120: the
-// code's exponent and significand moved to bf16's places (bias 7 against 127;
-// subnormal codes included). An exact product brings it back. The NaN code
-// comes out as 480; nan_codes finds it.
-__device__ __forceinline__ uint32_t e4m3_places(uint32_t high_bytes) {
-  return ((high_bytes >> 4) & 0x07f007f0u) | (high_bytes & 0x80008000u);
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 

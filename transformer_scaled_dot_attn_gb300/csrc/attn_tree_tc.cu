@@ -7,10 +7,17 @@
 // NB 128-key tiles in the tensor cores' layout:
 //   producer    TMA loads. bf16 caches: straight into the ring. e4m3 caches:
 //               the codes into a ring of their own, from which
-//   converters  (4 warps, one key row a thread) write the values code 2^e, each
-//               a bf16 number, into the ring. So the products see the cache's
-//               exact values, a code is converted once for all rows, and the
-//               softmax carries no scales.
+//   converters  (4 warps, one key row a thread) write f16 values into the
+//               ring, code 2^(e - top + 7) with `top` the largest scale of the
+//               part's keys: so a code is converted once for all rows, one
+//               conversion and one exact product for two codes, and the softmax
+//               carries no scales. f16 holds them exactly down to 2^-22 of the
+//               largest; below that they lose low bits, and 2^-33 becomes 0.
+//               (Exact bf16 values took five operations for two codes: 64 tokens
+//               with eight query heads a key head, d = 128: 119 us.)
+//               The queries are brought to f16 as well, each row to [2^14, 2^15)
+//               by a power of two, and the weights are f16 against a reference
+//               2^7 below the maximum, so that they reach down to 2^-31 of it.
 //   cleaner     (bf16) passes V tiles on; in tiles that reach the newest n
 //               positions it zeroes the rows past the sequence and values that
 //               are not finite (weight 0 times NaN is NaN). Rows that see such a
@@ -72,6 +79,8 @@ constexpr int kMaxRing = 8;
 
 struct TcShared {
   uint64_t q_full, q_empty;
+  uint64_t q_f16[2];                           // e4m3 caches: query tile g is in f16
+  uint64_t scanned;                            // e4m3 caches: the part's scales were looked at
   uint64_t full[kMaxRing], empty[kMaxRing];    // bf16 tiles: filled (TMA or converters), released by the issuers
   uint64_t clean[kMaxRing];                    // bf16 caches: the V tile in this place is clean
   uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];
@@ -79,6 +88,8 @@ struct TcShared {
   uint64_t pv_done[2], o_full[2], o_free[2], drain[2];
   uint32_t tmem_base;
   int abort_flag;
+  int ref[4][2];                               // e4m3 caches: largest scale byte of K and V, by part
+  int scan[4][4][2];                           // the converter warps' maxima, by part
   int odd[4];                                  // part + 1 whose newest positions hold values that are not finite
 };
 
@@ -125,6 +136,31 @@ __device__ __forceinline__ uint32_t raw_off(int r, int cc) {
   return r * D + (pc << 4);
 }
 
+// Two codes as f16 values times the pair of factors f.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t two, uint32_t f) {
+  uint32_t h, r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(f));
+  return r;
+}
+
+// The larger finite magnitude of a bf16 pair, as bf16 bits (0: none).
+__device__ __forceinline__ uint32_t finite_top(uint32_t w) {
+  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+  return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
+}
+
+__device__ __forceinline__ uint32_t to_f16(uint32_t w, float f) {
+  const float2 x = unpack_bf16x2(w);
+  return pack_f16x2(x.x * f, x.y * f);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2_pair(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_f16x2(lo, hi);
+}
+
 // The value (bf16 bits) at column c of a position, for the rare rows that add it themselves.
 template <int D, bool Q8>
 __device__ __forceinline__ float value_of(const TreeParams& p, int bh, int key, int c) {
@@ -156,6 +192,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, NQ);
+    mbar_init(&sh.scanned, 4);
     for (int s = 0; s < C::NB; ++s) {
       mbar_init(&sh.full[s], Q8 ? 128 : 1);
       mbar_init(&sh.empty[s], NQ);
@@ -166,6 +203,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       mbar_init(&sh.raw_empty[s], 128);
     }
     for (int g = 0; g < NQ; ++g) {
+      mbar_init(&sh.q_f16[g], 128);
       for (int u = 0; u < 2; ++u) {
         mbar_init(&sh.s_full[g][u], 1);
         mbar_init(&sh.p_full[g][u], 128);
@@ -202,9 +240,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lane_base + C::TM_O + g * D;
-    // scale 0: a tiny positive factor keeps -inf (masked) at weight 0
-    const float c = p.c != 0.f ? fabsf(p.c) : 1e-30f;
-    const uint64_t c2 = f2_pack(c, c);
+    // e4m3: weights against a reference this far below the maximum (log2 units)
+    constexpr float kLow = Q8 ? 7.f : 0.f;
 #pragma unroll 1
     while (ok && tree_next(p, kBN, walk, part)) {
       const int old = part.L - p.n;
@@ -213,7 +250,31 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       const bool idle = __all_sync(0xffffffffu, !real);  // this warp's rows do not exist
       const unsigned long long word = real ? tree_word(p, part.b, row) : 0ull;
       const int T = part.t1 - part.t0;
+      // scale 0: a tiny positive factor keeps -inf (masked) at weight 0
+      float c = fmaxf(fabsf(p.c), 1e-30f);
+      if constexpr (Q8) {
+        ok = __all_sync(0xffffffffu, guarded_wait(&sh.q_full, seg & 1, abort_flag, wd, kSiteQFull));
+        if (!ok) break;
+        uint8_t* tile = smem + C::OFF_Q + g * C::TILE;
+        uint4 w[D / 8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int cc = 0; cc < D / 8; ++cc) {
+          w[cc] = *reinterpret_cast<const uint4*>(tile + chunk_off<D>(r, cc));
+          top = max(top, max(max(finite_top(w[cc].x), finite_top(w[cc].y)), max(finite_top(w[cc].z), finite_top(w[cc].w))));
+        }
+        const uint32_t up = 268u - max(top >> 7, 15u);
+        const float f = __uint_as_float(up << 23);
+        c *= __uint_as_float((254u - up) << 23);
+#pragma unroll
+        for (int cc = 0; cc < D / 8; ++cc)
+          *reinterpret_cast<uint4*>(tile + chunk_off<D>(r, cc)) =
+              make_uint4(to_f16(w[cc].x, f), to_f16(w[cc].y, f), to_f16(w[cc].z, f), to_f16(w[cc].w, f));
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.q_f16[g]);
+      }
       float m_used = -INFINITY, l = 0.f;
+      uint64_t c2 = f2_pack(c, c);
 #pragma unroll 1
       for (int j = 0; j < T; ++j) {
         const int gi = done + j;
@@ -223,6 +284,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         ok = __all_sync(0xffffffffu, guarded_wait(&sh.s_full[g][u], ph, abort_flag, wd, kSiteSFull));
         if (!ok) break;
         tc_fence_after();
+        if (Q8 && j == 0) {  // the part's largest K scale is known by now
+          c = fmaxf(c * pow2_of_byte(sh.ref[seg & 3][0]) * 0x1p-7f, 1e-37f);
+          c2 = f2_pack(c, c);
+        }
         if (idle) {
           tc_fence_before();
           mbar_arrive(&sh.p_full[g][u]);
@@ -262,7 +327,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           m_used = m_new;
           moved = true;
         }
-        const float m_ref = m_used == -INFINITY ? 0.f : m_used;  // nothing seen yet: weights 0
+        const float m_ref = m_used == -INFINITY ? 0.f : m_used - kLow;  // nothing seen yet: weights 0
         const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
         uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll
@@ -275,7 +340,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             float x0, x1;
             f2_unpack(x2, x0, x1);
             const uint64_t p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
-            pk[i] = pack_bf16x2_pair(p2);
+            pk[i] = Q8 ? pack_f16x2_pair(p2) : pack_bf16x2_pair(p2);
             if (i & 1) acc1 = add2(acc1, p2);
             else acc0 = add2(acc0, p2);
           }
@@ -303,8 +368,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       tc_fence_after();
       if (!idle) {
         const bool odd = *static_cast<volatile int*>(&sh.odd[seg & 3]) == seg + 1;
-        if (m_used == -INFINITY && l != 0.f) m_used = 0.f;  // only NaN scores: against the reference 0
-        const float inv = m_used == -INFINITY ? 0.f : 1.f / l;
+        const float unit_v = Q8 ? pow2_of_byte(sh.ref[seg & 3][1]) * 0x1p-7f : 1.f;
+        // the reference of l and O (only NaN scores: 0)
+        m_used = m_used == -INFINITY ? (l != 0.f ? 0.f : -INFINITY) : m_used - kLow;
+        const float inv = m_used == -INFINITY ? 0.f : unit_v / l;
         const size_t out = static_cast<size_t>(part.bh) * p.rows + row;
         const size_t at = static_cast<size_t>(part.slot) * p.block_rows + g * 128 + r;
         // (not unrolled: each turn's loads and stores are independent of the others')
@@ -335,6 +402,9 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           } else {
             uint4* dst = reinterpret_cast<uint4*>(p.part + at * D + q * 16);
             // (a row that saw nothing: its products are 0)
+            if (Q8)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit_v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
@@ -359,10 +429,33 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     while (ok && tree_next(p, kBN, walk, part)) {
       const int old = part.L - p.n, T = part.t1 - part.t0;
       const size_t row0 = static_cast<size_t>(part.bh) * p.m;
-      int bytes[2] = {127, 127};
+      const int key_end = min(part.L, part.t1 * kBN);
+      // the largest scales of the part's keys
+      int top[2] = {0, 0};
+#pragma unroll 4
+      for (int key = part.t0 * kBN + r; key < key_end; key += kBN) {
+        top[0] = max(top[0], static_cast<int>(__ldg(p.k_exp + row0 + key)));
+        top[1] = max(top[1], static_cast<int>(__ldg(p.v_exp + row0 + key)));
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        top[u] = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top[u])));
+        if (lane == 0) sh.scan[seg & 3][warp - C::CONV][u] = top[u];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.scanned);
+      ok = __all_sync(0xffffffffu, guarded_wait(&sh.scanned, seg & 1, abort_flag, wd, kSiteKFull));
+      if (!ok) break;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int* of = &sh.scan[seg & 3][0][u];
+        top[u] = max(max(of[0], of[2]), max(of[4], of[6]));
+        if (r == 0) sh.ref[seg & 3][u] = top[u];
+      }
+      int bytes[2] = {0, 0};
       auto scales = [&](int j) {  // of the tile's K and V row, read a tile ahead
         const int key = (part.t0 + j) * kBN + r;
-        if (j < T && key < part.L) {
+        if (key < key_end) {
           bytes[0] = __ldg(p.k_exp + row0 + key);
           bytes[1] = __ldg(p.v_exp + row0 + key);
         }
@@ -370,7 +463,14 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       scales(0);
 #pragma unroll 1
       for (int j = 0; ok && j < T; ++j) {
-        const int cur[2] = {bytes[0], bytes[1]};
+        // 2^(e - top + 7) in f16, below 2^-14 as the subnormal numbers it has
+        uint32_t f2[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int e = bytes[u] - top[u] + 7;
+          const uint32_t f = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+          f2[u] = f | (f << 16);
+        }
         scales(j + 1);
         const int key = (part.t0 + j) * kBN + r;
         const bool tail = (part.t0 + j + 1) * kBN > old;
@@ -384,40 +484,39 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           if (!ok) break;
           const uint8_t* src = smem + C::OFF_R + rs * C::RAW;
           uint8_t* dst = smem + C::OFF_B + bs * C::TILE;
-          // code 2^e: the places' 2^-120, then 2^(120 + e); beyond bf16's 2^127 in two steps
-          const int up = 120 + (kv ? cur[1] : cur[0]) - 127;
-          const uint32_t f = static_cast<uint32_t>(127 + min(up, 127)) << 7;
-          const uint32_t f2 = f | (f << 16);
-          const uint32_t rest = static_cast<uint32_t>(127 + max(up - 127, 0)) << 7;
-          const uint32_t rest2 = rest | (rest << 16);
-          const bool zero = kv == 1 && key >= part.L;  // what lies past the sequence is anyone's
-          uint32_t nans = 0;
+          const uint32_t f = f2[kv];
+          if (kv == 1 && tail) {
+            // Rows past the sequence are anyone's: zeros. NaN codes become zeros
+            // too (a weight of 0 would make them NaN for rows that do not see
+            // them); the rows that do see them add them at the end.
+            const bool zero = key >= part.L;
+            bool odd = false;
+            for (int cc = 0; cc < D / 16; ++cc) {
+              const uint4 w4 = *reinterpret_cast<const uint4*>(src + raw_off<D>(r, cc));
+              uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+              uint32_t o[8];
 #pragma unroll
-          for (int cc = 0; cc < D / 16; ++cc) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(src + raw_off<D>(r, cc));
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              nans |= nan_codes(w[i]);
-              o[2 * i] = mul_bf16x2(e4m3_places(__byte_perm(w[i], 0, 0x1404)), f2);
-              o[2 * i + 1] = mul_bf16x2(e4m3_places(__byte_perm(w[i], 0, 0x3424)), f2);
-              if (up > 127) {
-                o[2 * i] = mul_bf16x2(o[2 * i], rest2);
-                o[2 * i + 1] = mul_bf16x2(o[2 * i + 1], rest2);
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t n = nan_codes(w[i]) & 0x80808080u;
+                odd |= n != 0;
+                w[i] = zero ? 0u : w[i] & ~((n >> 7) * 0xffu);
+                o[2 * i] = codes_f16(w[i] & 0xffffu, f);
+                o[2 * i + 1] = codes_f16(w[i] >> 16, f);
               }
-              if (zero) o[2 * i] = o[2 * i + 1] = 0u;
+              *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
-            *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          if ((nans & 0x80808080u) != 0 && !zero) {
-            if (kv == 1 && tail) {
-              sh.odd[seg & 3] = seg + 1;  // the rows that see it add it (480 2^e stands in for it)
-            } else {
-              for (int x = 0; x < D; ++x)
-                if ((src[raw_off<D>(r, x >> 4) + (x & 15)] & 0x7fu) == 0x7fu)
-                  *reinterpret_cast<uint16_t*>(dst + chunk_off<D>(r, x >> 3) + (x & 7) * 2) = 0x7fc0u;
+            if (odd && !zero) sh.odd[seg & 3] = seg + 1;
+          } else {
+#pragma unroll
+            for (int cc = 0; cc < D / 16; ++cc) {
+              const uint4 w = *reinterpret_cast<const uint4*>(src + raw_off<D>(r, cc));
+              *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc)) =
+                  make_uint4(codes_f16(w.x & 0xffffu, f), codes_f16(w.x >> 16, f), codes_f16(w.y & 0xffffu, f),
+                             codes_f16(w.y >> 16, f));
+              *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc + 1)) =
+                  make_uint4(codes_f16(w.z & 0xffffu, f), codes_f16(w.z >> 16, f), codes_f16(w.w & 0xffffu, f),
+                             codes_f16(w.w >> 16, f));
             }
           }
           fence_proxy_async_smem();
@@ -477,8 +576,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       // ---------------------------------------------------------- issuer of query tile g
       const int g = warp - C::ISSUER;
       if (lane == 0) {
-        const uint32_t idesc_s = idesc_bf16_f32(128, kBN, false, false) | (p.c < 0.f ? (1u << 13) : 0u);
-        const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+        constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // operand formats of the descriptor; f16 is 0
+        const uint32_t idesc_s =
+            (idesc_bf16_f32(128, kBN, false, false) & ~(Q8 ? kBf16 : 0u)) | (p.c < 0.f ? (1u << 13) : 0u);
+        const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true) & ~(Q8 ? kBf16 : 0u);
         const uint32_t sq = smem_u32(smem + C::OFF_Q) + g * C::TILE;
         const uint32_t sb = smem_u32(smem + C::OFF_B);
         const uint32_t t_s = tmem + g * C::NS * kBN, t_o = tmem + C::TM_O + g * D;
@@ -499,7 +600,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll 1
         while (ok && tree_next(p, kBN, walk, part)) {
           const int T = part.t1 - part.t0;
-          ok = guarded_wait(&sh.q_full, seg & 1, abort_flag, wd, kSiteQFull) && scores(done);
+          ok = guarded_wait(Q8 ? &sh.q_f16[g] : &sh.q_full, seg & 1, abort_flag, wd, kSiteQFull) && scores(done);
           for (int j = 0; ok && j < T; ++j) {
             const int gi = done + j, h = 2 * gi + 1, st = h % C::NB;
             const int u = C::NS == 2 ? (gi & 1) : 0;

@@ -95,19 +95,16 @@ def tree_step(q, k, v, lens, words, scale):
     A, lse, S = o.clone(), torch.full((B, h, n), -math.inf, dtype=F64), torch.zeros(B, h, n, dtype=F64)
     for b in range(B):
         L = lens[b]
+        if L == 0:
+            continue
         see = visible(n, L, None if words is None else words[b])
         for hd in range(h):
             kk, vv, qq = k[b, hd // group, :L].to(F64), v[b, hd // group, :L].to(F64), q[b, hd].to(F64)
-            for i in range(n):
-                j = see[i].nonzero()[:, 0]
-                if j.numel() == 0:
-                    continue
-                x = scale * (kk[j] @ qq[i])
-                lse[b, hd, i] = torch.logsumexp(x, 0)
-                p = torch.exp(x - lse[b, hd, i])
-                o[b, hd, i] = p @ vv[j]
-                A[b, hd, i] = p @ vv[j].abs()
-                S[b, hd, i] = (abs(scale) * (kk[j].abs() @ qq[i].abs())).amax()
+            x = torch.where(see, scale * (qq @ kk.T), -math.inf)
+            lse[b, hd] = torch.logsumexp(x, -1)
+            p = torch.where(see, torch.exp(x - lse[b, hd, :, None]), 0.0)
+            o[b, hd], A[b, hd] = p @ vv, p @ vv.abs()
+            S[b, hd] = torch.where(see, abs(scale) * (qq.abs() @ kk.abs().T), 0.0).amax(-1)
     return o, lse, A, S
 
 

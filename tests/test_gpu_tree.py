@@ -64,6 +64,23 @@ def test_matches_the_definition(case, quantised):
     R.check_tree(o, lse, R.tree_step(q, k, v, lens or [m] * B, words, scale))
 
 
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("n,group,d", [(64, 8, 128), (64, 1, 128), (8, 1, 128), (64, 4, 64), (33, 1, 32), (16, 1, 64)])
+def test_long_caches(n, group, d, quantised):
+    """Hundreds of key tiles through every ring, many times, in batches of different lengths."""
+    B, hkv, m = 3, 4, 20011
+    q = R.bf16(B, hkv * group, n, d, seed=7)
+    c, (k, v) = caches(B, hkv, m, d, quantised, 11)
+    words = R.random_tree(B, n, 3)
+    lens = [20011, 5000, 17777]
+    for _ in range(20):
+        o, lse = run(q, c, lens, words, d ** -0.5)
+    for b, g in ((0, 0), (1, 2), (2, 3)):
+        hs = slice(g * group, (g + 1) * group)
+        ref = R.tree_step(q[b:b + 1, hs], k[b:b + 1, g:g + 1], v[b:b + 1, g:g + 1], [lens[b]], [words[b]], d ** -0.5)
+        R.check_tree(o[b:b + 1, hs], lse[b:b + 1, hs], ref)
+
+
 @pytest.mark.parametrize("n", [1, 2, 7, 8, 15, 16, 17, 31, 32, 33, 48, 63, 64])
 def test_every_row_count(n):
     """Rows around the tiles' edges, lengths around the key tiles' edges."""

@@ -48,15 +48,18 @@ struct Tc {
   static constexpr uint32_t TILE = kBN * D * 2u;           // a K, V or Q tile in bf16
   static constexpr uint32_t BOX = kBN * ATOM * 2u;
   static constexpr uint32_t RAW = Q8 ? kBN * D : 0;        // a tile of codes
-  static constexpr int NB = Q8 ? (D == 128 ? 3 : 6) : (D == 128 && NQ == 2 ? 5 : 6);          // ring of bf16 tiles
+  // Ring of bf16 tiles. For bf16 caches an even number, so that a place always
+  // holds K or always V: the cleaner waits for V tiles only, and a place that K
+  // passes through could complete two phases between its looks (a wait tells
+  // phases apart by their parity alone).
+  static constexpr int NB = Q8 ? (D == 128 ? 3 : 6) : (D == 128 && NQ == 2 ? 4 : 6);
+  static_assert(Q8 || NB % 2 == 0, "the cleaner's waits");
   static constexpr int NR = Q8 ? (D == 128 ? (NQ == 2 ? 4 : 6) : 8) : 1;     // ring of code tiles
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_B = NQ * TILE;
   static constexpr uint32_t OFF_R = OFF_B + NB * TILE;
   static constexpr uint32_t SMEM = OFF_R + (Q8 ? NR * RAW : 0) + 1024;       // + alignment slack
   static_assert(SMEM <= 227u * 1024u, "shared memory");
-  // how often ring tile h's place held a V tile before (an odd ring holds one every other pass)
-  __device__ static constexpr int v_pass(int h) { return NB % 2 == 0 ? h / NB : h / NB / 2; }
   static constexpr int NS = NQ == 1 ? 2 : 1;               // S buffers of a query tile
   static constexpr int TM_O = NQ * NS * kBN;               // TMEM: S buffers, then O
   static constexpr int TMEM = TM_O + NQ * D <= 256 ? 256 : 512;
@@ -609,8 +612,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             ok = guarded_wait(&sh.p_full[g][u], (C::NS == 2 ? gi >> 1 : gi) & 1, abort_flag, wd, kSitePFull);
             // the previous part's O has been read
             if (ok && j == 0 && seg > 0) ok = guarded_wait(&sh.o_free[g], (seg - 1) & 1, abort_flag, wd, kSiteOFull);
-            if (ok) ok = guarded_wait(Q8 ? &sh.full[st] : &sh.clean[st], Q8 ? (h / C::NB) & 1 : C::v_pass(h) & 1,
-                                      abort_flag, wd, kSiteVFull);
+            if (ok) ok = guarded_wait(Q8 ? &sh.full[st] : &sh.clean[st], (h / C::NB) & 1, abort_flag, wd, kSiteVFull);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -639,7 +641,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll 1
         for (int j = 0; ok && j < T; ++j) {
           const int h = 2 * (done + j) + 1, st = h % C::NB;
-          ok = __all_sync(0xffffffffu, guarded_wait(&sh.full[st], (h / C::NB) & 1, abort_flag, wd, kSiteVFull));
+          ok = guarded_wait(&sh.full[st], (h / C::NB) & 1, abort_flag, wd, kSiteVFull);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const int k0 = (part.t0 + j) * kBN;
           if (k0 + kBN > old) {

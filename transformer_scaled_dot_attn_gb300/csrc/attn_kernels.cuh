@@ -325,7 +325,7 @@ struct TreeParams {
   const __nv_bfloat16* q;          // [B h_kv][rows][d]: the query heads of a key head are neighbours
   __nv_bfloat16* o;                // like q
   float* lse;                      // [B h_kv][rows] or nullptr
-  float* part;                     // [slots][block rows][d] fp32 partial O (not divided)
+  float* part;                     // fp32 partial O (not divided) of each slot: block rows x d
   float* part_ml;                  // [slots][block rows][2]: maximum (log2 units) and sum
   const unsigned long long* tree;  // [B][n] or nullptr (causal)
   const int* kv_len;               // [B] or nullptr

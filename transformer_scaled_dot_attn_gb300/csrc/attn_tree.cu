@@ -580,19 +580,20 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   }
 }
 
-// Joins the parts of a unit's rows (one warp a row), rescaled to the common
-// maximum and added in the line's order. Grid: x = unit, y = 8 rows of its block.
-template <int D>
-__global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p, int bn, int grid, int least) {
-  const TreeLine l = tree_line(p, bn, grid, least);
-  grid_wait();  // the parts are written
-  const int unit = blockIdx.x, lane = threadIdx.x & 31;
+// Joins the parts of a unit's rows, rescaled to the common maximum and added in
+// the line's order. Partial O lies as the step's threads write it without gaps:
+//   mma.sync kernel   [slot][row][d]: a warp joins one row, lanes over the columns;
+//   tcgen05 kernel    [slot][d / 4][row][4]: a lane joins one row, warps over the columns.
+struct UnitParts {
+  int first, parts;  // the first CTA that holds a part of the unit, and how many do
+};
+
+// Every lane of a warp calls this.
+__device__ __forceinline__ UnitParts unit_parts(const TreeParams& p, const TreeLine& l, int unit, int bn) {
+  const int lane = threadIdx.x & 31;
   const int b = unit / l.per_seq, idx = unit - b * l.per_seq;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int row = (idx % p.row_blocks) * p.block_rows + r;
-  if (r >= p.block_rows || row >= p.rows) return;
-  long long first = 0;  // the unit's place on the line
   const int tiles = tiles_of(tree_len(p, b), bn);
+  long long first = 0;  // the unit's place on the line
   if (p.kv_len == nullptr) {
     first = static_cast<long long>(b) * tiles;
   } else {
@@ -604,33 +605,90 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p
   // the CTAs that hold its first and its last tile: the largest c with U c / ctas at or before them
   const int c0 = static_cast<int>(((first + 1) * l.ctas - 1) / l.U);
   const int c1 = static_cast<int>(((first + tiles) * l.ctas - 1) / l.U);
-  if (c0 == c1) return;  // one part: its CTA wrote the results
+  return UnitParts{c0, c1 - c0 + 1};
+}
+
+// Grid: x = unit, y = 8 rows of its block (a warp a row).
+template <int D>
+__global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p, int bn, int grid, int least) {
+  const TreeLine l = tree_line(p, bn, grid, least);
+  const int unit = blockIdx.x, lane = threadIdx.x & 31;
+  const UnitParts u = unit_parts(p, l, unit, bn);
+  grid_wait();  // the parts are written
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int row = (unit % p.row_blocks) * p.block_rows + r;
+  if (u.parts == 1 || r >= p.block_rows || row >= p.rows) return;  // one part: its CTA wrote the results
   const size_t step = static_cast<size_t>(p.block_rows);
-  const size_t at = (static_cast<size_t>(unit) + c0) * step + r;
-  const int parts = c1 - c0 + 1;
+  const size_t at = (static_cast<size_t>(unit) + u.first) * step + r;
   float M = -INFINITY;
-  for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.part_ml[2 * (at + s * step)]);
+  for (int s = lane; s < u.parts; s += 32) M = fmaxf(M, p.part_ml[2 * (at + s * step)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   constexpr int PER = D / 32;
   float o[PER], sum = 0.f;
 #pragma unroll
-  for (int u = 0; u < PER; ++u) o[u] = 0.f;
+  for (int i = 0; i < PER; ++i) o[i] = 0.f;
   if (M != -INFINITY) {
 #pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
+    for (int s = 0; s < u.parts; ++s) {
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + s * step));
       const float w = ex2_approx(ml.x - M);  // 0 for a part without a key that the row sees
       sum = fmaf(w, ml.y, sum);
 #pragma unroll
-      for (int u = 0; u < PER; ++u) o[u] = fmaf(w, p.part[(at + s * step) * D + lane + 32 * u], o[u]);
+      for (int i = 0; i < PER; ++i) o[i] = fmaf(w, p.part[(at + s * step) * D + lane + 32 * i], o[i]);
     }
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / sum;
-  const size_t out = (static_cast<size_t>(b) * p.h_kv + idx / p.row_blocks) * p.rows + row;
+  const size_t out = static_cast<size_t>(unit / p.row_blocks) * p.rows + row;
 #pragma unroll
-  for (int u = 0; u < PER; ++u) p.o[out * D + lane + 32 * u] = __float2bfloat16_rn(o[u] * inv);
+  for (int i = 0; i < PER; ++i) p.o[out * D + lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
   if (lane == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
+}
+
+// Grid: x = unit, y = 32 rows of its block (a lane a row); each of the 8 warps D / 8 columns.
+template <int D>
+__global__ void __launch_bounds__(256) attn_tree_tc_merge_kernel(const TreeParams p, int bn, int grid, int least) {
+  const TreeLine l = tree_line(p, bn, grid, least);
+  const int unit = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const UnitParts u = unit_parts(p, l, unit, bn);
+  grid_wait();
+  const int r = blockIdx.y * 32 + lane;
+  const int row = (unit % p.row_blocks) * p.block_rows + r;
+  if (u.parts == 1 || row >= p.rows) return;
+  const size_t step = static_cast<size_t>(p.block_rows), slot = static_cast<size_t>(unit) + u.first;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + slot * step + r;
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < u.parts; ++s) M = fmaxf(M, ml[s * step].x);
+  constexpr int C4 = D / 32;  // groups of four columns
+  float4 o[C4];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < C4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M != -INFINITY) {
+    const float4* part = reinterpret_cast<const float4*>(p.part) + (slot * (D / 4) + warp * C4) * step + r;
+#pragma unroll 2
+    for (int s = 0; s < u.parts; ++s) {
+      const float2 x = ml[s * step];
+      const float w = ex2_approx(x.x - M);
+      sum = fmaf(w, x.y, sum);
+#pragma unroll
+      for (int i = 0; i < C4; ++i) {
+        const float4 v = part[(static_cast<size_t>(s) * (D / 4) + i) * step];
+        o[i].x = fmaf(w, v.x, o[i].x);
+        o[i].y = fmaf(w, v.y, o[i].y);
+        o[i].z = fmaf(w, v.z, o[i].z);
+        o[i].w = fmaf(w, v.w, o[i].w);
+      }
+    }
+  }
+  const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+  const size_t out = static_cast<size_t>(unit / p.row_blocks) * p.rows + row;
+  uint2* dst = reinterpret_cast<uint2*>(p.o + out * D + warp * (D / 8));
+#pragma unroll
+  for (int i = 0; i < C4; ++i)
+    dst[i] = make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
+  if (warp == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
 }
 
 int small_ctas(int d, bool quantised) {
@@ -684,11 +742,15 @@ cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMa
   else e = launch_small_rows<D, false>(plan.grid, tk, tv, p, stream);
   if (e != cudaSuccess || plan.by_unit) return e;
   const unsigned units = static_cast<unsigned>(p.B) * p.h_kv * p.row_blocks;
-  const int warps = p.block_rows < 8 ? p.block_rows : 8;
   prof_begin(kKindTreeMerge, stream);
-  e = launch_dependent(attn_tree_merge_kernel<D>, dim3(units, static_cast<unsigned>((p.block_rows + 7) / 8)),
-                       dim3(static_cast<unsigned>(warps * 32)), stream, p, plan.tile, plan.grid,
-                       plan.tc ? kTreeLeastTc : kTreeLeast);
+  if (plan.tc) {
+    e = launch_dependent(attn_tree_tc_merge_kernel<D>, dim3(units, static_cast<unsigned>(p.block_rows / 32)), dim3(256),
+                         stream, p, plan.tile, plan.grid, kTreeLeastTc);
+  } else {
+    const int warps = p.block_rows < 8 ? p.block_rows : 8;
+    e = launch_dependent(attn_tree_merge_kernel<D>, dim3(units, static_cast<unsigned>((p.block_rows + 7) / 8)),
+                         dim3(static_cast<unsigned>(warps * 32)), stream, p, plan.tile, plan.grid, kTreeLeast);
+  }
   prof_end(kKindTreeMerge, stream);
   return e;
 }

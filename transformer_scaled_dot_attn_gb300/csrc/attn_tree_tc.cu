@@ -87,14 +87,22 @@ struct TcShared {
   uint64_t full[kMaxRing], empty[kMaxRing];    // bf16 tiles: filled (TMA or converters), released by the issuers
   uint64_t clean[kMaxRing];                    // bf16 caches: the V tile in this place is clean
   uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];
-  uint64_t s_full[2][2], p_full[2][2];         // query tile, S buffer
+  uint64_t s_full[2][2];                       // query tile, S buffer
+  uint64_t p_full[2][2][2];                    // query tile, S buffer, half of the tile's keys
   uint64_t pv_done[2], o_full[2], o_free[2], drain[2];
+  uint64_t turn[2];                            // two query tiles: their exponentials alternate
   uint32_t tmem_base;
   int abort_flag;
   int ref[4][2];                               // e4m3 caches: largest scale byte of K and V, by part
   int scan[4][4][2];                           // the converter warps' maxima, by part
   int odd[4];                                  // part + 1 whose newest positions hold values that are not finite
 };
+
+// One arrival for the warp, after everything its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 
 // Waits without looking at the abort flag: copies and products in flight must
 // finish before the CTA's memory goes away.
@@ -197,24 +205,26 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     mbar_init(&sh.q_empty, NQ);
     mbar_init(&sh.scanned, 4);
     for (int s = 0; s < C::NB; ++s) {
-      mbar_init(&sh.full[s], Q8 ? 128 : 1);
+      mbar_init(&sh.full[s], Q8 ? 4 : 1);
       mbar_init(&sh.empty[s], NQ);
       mbar_init(&sh.clean[s], 1);
     }
     for (int s = 0; s < C::NR; ++s) {
       mbar_init(&sh.raw_full[s], 1);
-      mbar_init(&sh.raw_empty[s], 128);
+      mbar_init(&sh.raw_empty[s], 4);
     }
     for (int g = 0; g < NQ; ++g) {
-      mbar_init(&sh.q_f16[g], 128);
+      mbar_init(&sh.q_f16[g], 4);
       for (int u = 0; u < 2; ++u) {
         mbar_init(&sh.s_full[g][u], 1);
-        mbar_init(&sh.p_full[g][u], 128);
+        mbar_init(&sh.p_full[g][u][0], 4);
+        mbar_init(&sh.p_full[g][u][1], 4);
       }
       mbar_init(&sh.pv_done[g], 1);
       mbar_init(&sh.o_full[g], 1);
-      mbar_init(&sh.o_free[g], 128);
+      mbar_init(&sh.o_free[g], 4);
       mbar_init(&sh.drain[g], 1);
+      mbar_init(&sh.turn[g], 4);
     }
     sh.abort_flag = 0;
     for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
@@ -274,7 +284,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           *reinterpret_cast<uint4*>(tile + chunk_off<D>(r, cc)) =
               make_uint4(to_f16(w[cc].x, f), to_f16(w[cc].y, f), to_f16(w[cc].z, f), to_f16(w[cc].w, f));
         fence_proxy_async_smem();
-        mbar_arrive(&sh.q_f16[g]);
+        warp_arrive(&sh.q_f16[g]);
       }
       float m_used = -INFINITY, l = 0.f;
       uint64_t c2 = f2_pack(c, c);
@@ -292,8 +302,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           c2 = f2_pack(c, c);
         }
         if (idle) {
+          if (NQ == 2) warp_arrive(&sh.turn[g ^ 1]);
           tc_fence_before();
-          mbar_arrive(&sh.p_full[g][u]);
+          warp_arrive(&sh.p_full[g][u][0]);
+          warp_arrive(&sh.p_full[g][u][1]);
           continue;
         }
         uint32_t s[4][32];
@@ -332,38 +344,49 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         const float m_ref = m_used == -INFINITY ? 0.f : m_used - kLow;  // nothing seen yet: weights 0
         const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
-        uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t x2 =
-                fma2(f2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, nm2);
-            float x0, x1;
-            f2_unpack(x2, x0, x1);
-            const uint64_t p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
-            pk[i] = Q8 ? pack_f16x2_pair(p2) : pack_bf16x2_pair(p2);
-            if (i & 1) acc1 = add2(acc1, p2);
-            else acc0 = add2(acc0, p2);
-          }
-          tmem_st16(t_s + q * 16, pk);
+        if (NQ == 2 && (g == 1 || gi > 0)) {
+          // the exponentials of the two query tiles take turns (0, 1, 0, 1, ...), so
+          // that one tile's overlap the other's products
+          ok = __all_sync(0xffffffffu, guarded_wait(&sh.turn[g], (g == 1 ? gi : gi - 1) & 1, abort_flag, wd, kSiteExpTurn));
+          if (!ok) break;
         }
-        float a0, a1, a2, a3;
-        f2_unpack(acc0, a0, a1);
-        f2_unpack(acc1, a2, a3);
-        l = l * alpha + ((a0 + a1) + (a2 + a3));
-        tmem_st_wait();
         if (j > 0 && __any_sync(0xffffffffu, moved)) {
           // the products so far are in O (with two S buffers the scores do not show that)
           ok = __all_sync(0xffffffffu, guarded_wait(&sh.pv_done[g], (gi - 1) & 1, abort_flag, wd, kSitePFull));
           if (!ok) break;
           tc_fence_after();
           tc_rescale<D>(t_o, alpha);
-          tmem_st_wait();
+          l *= alpha;
         }
-        tc_fence_before();
-        mbar_arrive(&sh.p_full[g][u]);
+        // weights of 64 keys, then of the other 64, whose products start meanwhile
+        uint64_t acc0 = f2_pack(l, 0.f), acc1 = f2_pack(0.f, 0.f);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int q = 2 * half; q < 2 * half + 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t x2 =
+                  fma2(f2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, nm2);
+              float x0, x1;
+              f2_unpack(x2, x0, x1);
+              const uint64_t p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
+              pk[i] = Q8 ? pack_f16x2_pair(p2) : pack_bf16x2_pair(p2);
+              if (i & 1) acc1 = add2(acc1, p2);
+              else acc0 = add2(acc0, p2);
+            }
+            tmem_st16(t_s + q * 16, pk);
+          }
+          if (NQ == 2 && half == 1) warp_arrive(&sh.turn[g ^ 1]);
+          tmem_st_wait();
+          tc_fence_before();
+          warp_arrive(&sh.p_full[g][u][half]);
+        }
+        float a0, a1, a2, a3;
+        f2_unpack(acc0, a0, a1);
+        f2_unpack(acc1, a2, a3);
+        l = (a0 + a1) + (a2 + a3);
       }
       if (ok)
         ok = __all_sync(0xffffffffu, guarded_wait(&sh.o_full[g], seg & 1, abort_flag, wd, kSiteOFull));
@@ -376,7 +399,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         m_used = m_used == -INFINITY ? (l != 0.f ? 0.f : -INFINITY) : m_used - kLow;
         const float inv = m_used == -INFINITY ? 0.f : unit_v / l;
         const size_t out = static_cast<size_t>(part.bh) * p.rows + row;
-        const size_t at = static_cast<size_t>(part.slot) * p.block_rows + g * 128 + r;
+        const int at = g * 128 + r;  // row of the block
         // (not unrolled: each turn's loads and stores are independent of the others')
 #pragma unroll 1
         for (int q = 0; q < D / 16; ++q) {
@@ -403,24 +426,27 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.part + at * D + q * 16);
-            // (a row that saw nothing: its products are 0)
-            if (Q8)
+            // Four columns of all rows side by side: a warp's rows are one run of
+            // 512 bytes. (A row that saw nothing: its products are 0.)
+            float4* dst = reinterpret_cast<float4*>(p.part) +
+                          (static_cast<size_t>(part.slot) * (D / 4) + q * 4) * p.block_rows + at;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit_v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 4; ++i)
+              dst[static_cast<size_t>(i) * p.block_rows] =
+                  make_float4(__uint_as_float(o[4 * i]) * unit_v, __uint_as_float(o[4 * i + 1]) * unit_v,
+                              __uint_as_float(o[4 * i + 2]) * unit_v, __uint_as_float(o[4 * i + 3]) * unit_v);
           }
         }
         if (real) {
           if (!part.whole)
-            *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_used, l);
+            *reinterpret_cast<float2*>(p.part_ml + 2 * (static_cast<size_t>(part.slot) * p.block_rows + at)) =
+                make_float2(m_used, l);
           else if (p.lse != nullptr)
             p.lse[out] = m_used == -INFINITY ? -INFINITY : (m_used + log2f(l)) * kTreeLn2;
         }
       }
       tc_fence_before();
-      mbar_arrive(&sh.o_free[g]);
+      warp_arrive(&sh.o_free[g]);
       done += T;
       ++seg;
     }
@@ -523,8 +549,11 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(&sh.full[bs]);
-          mbar_arrive(&sh.raw_empty[rs]);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.full[bs]);
+            mbar_arrive(&sh.raw_empty[rs]);
+          }
         }
       }
       done += T;
@@ -586,9 +615,12 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const uint32_t sq = smem_u32(smem + C::OFF_Q) + g * C::TILE;
         const uint32_t sb = smem_u32(smem + C::OFF_B);
         const uint32_t t_s = tmem + g * C::NS * kBN, t_o = tmem + C::TM_O + g * D;
-        auto scores = [&](int gi) {  // S of the walk's tile gi
-          const int h = 2 * gi, st = h % C::NB, u = C::NS == 2 ? (gi & 1) : 0;
-          if (!guarded_wait(&sh.full[st], (h / C::NB) & 1, abort_flag, wd, kSiteKFull)) return false;
+        auto k_ready = [&](int gi) {
+          const int h = 2 * gi;
+          return guarded_wait(&sh.full[h % C::NB], (h / C::NB) & 1, abort_flag, wd, kSiteKFull);
+        };
+        auto scores = [&](int gi) {  // S of the walk's tile gi, whose K tile is there
+          const int st = 2 * gi % C::NB, u = C::NS == 2 ? (gi & 1) : 0;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -598,32 +630,40 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           }
           mma_commit(&sh.s_full[g][u]);
           mma_commit(&sh.empty[st]);
-          return true;
         };
 #pragma unroll 1
         while (ok && tree_next(p, kBN, walk, part)) {
           const int T = part.t1 - part.t0;
-          ok = guarded_wait(Q8 ? &sh.q_f16[g] : &sh.q_full, seg & 1, abort_flag, wd, kSiteQFull) && scores(done);
+          ok = guarded_wait(Q8 ? &sh.q_f16[g] : &sh.q_full, seg & 1, abort_flag, wd, kSiteQFull) && k_ready(done);
+          if (ok) scores(done);
           for (int j = 0; ok && j < T; ++j) {
             const int gi = done + j, h = 2 * gi + 1, st = h % C::NB;
             const int u = C::NS == 2 ? (gi & 1) : 0;
-            if (C::NS == 2 && j + 1 < T && !(ok = scores(gi + 1))) break;
+            const uint32_t ph = (C::NS == 2 ? gi >> 1 : gi) & 1;
+            if (C::NS == 2 && j + 1 < T) {
+              if (!(ok = k_ready(gi + 1))) break;
+              scores(gi + 1);
+            }
             if (j + 1 == T) mma_commit(&sh.q_empty);  // this part's last scores are on their way
-            ok = guarded_wait(&sh.p_full[g][u], (C::NS == 2 ? gi >> 1 : gi) & 1, abort_flag, wd, kSitePFull);
+            // what is there long before the weights is waited for first
+            ok = guarded_wait(Q8 ? &sh.full[st] : &sh.clean[st], (h / C::NB) & 1, abort_flag, wd, kSiteVFull);
+            if (ok && C::NS == 1 && j + 1 < T) ok = k_ready(gi + 1);
             // the previous part's O has been read
             if (ok && j == 0 && seg > 0) ok = guarded_wait(&sh.o_free[g], (seg - 1) & 1, abort_flag, wd, kSiteOFull);
-            if (ok) ok = guarded_wait(Q8 ? &sh.full[st] : &sh.clean[st], (h / C::NB) & 1, abort_flag, wd, kSiteVFull);
-            if (!ok) break;
-            tc_fence_after();
+            for (int half = 0; ok && half < 2; ++half) {
+              if (!(ok = guarded_wait(&sh.p_full[g][u][half], ph, abort_flag, wd, kSitePFull))) break;
+              tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kBN / 16; ++k)
-              mma_ts(t_o, t_s + u * kBN + k * 8,
-                     smem_desc(sb + st * C::TILE + k * 16 * C::ATOM * 2, C::BOX, C::SBO, C::SWZ), idesc_o,
-                     (j > 0 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < kBN / 32; ++k)
+                mma_ts(t_o, t_s + u * kBN + half * 32 + k * 8,
+                       smem_desc(sb + st * C::TILE + (half * 4 + k) * 16 * C::ATOM * 2, C::BOX, C::SBO, C::SWZ), idesc_o,
+                       (j > 0 || half > 0 || k > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
             mma_commit(&sh.empty[st]);
             mma_commit(&sh.pv_done[g]);
             if (j + 1 == T) mma_commit(&sh.o_full[g]);
-            if (C::NS == 1 && j + 1 < T) ok = scores(gi + 1);
+            if (C::NS == 1 && j + 1 < T) scores(gi + 1);
           }
           done += T;
           ++seg;

@@ -102,21 +102,23 @@ bool make_map3(CUtensorMap* map, const void* base, long long d0, long long d1, l
   return r == CUDA_SUCCESS;
 }
 
-// 3-D map over a [BH, S, d] array of 8-bit codes: box = (d, box_rows, 1 head),
-// swizzled over the row's d bytes (d = 32: not).
-bool make_code_map(CUtensorMap* map, const void* base, long long BH, long long S, int d, int box_rows) {
+// 3-D map over a [BH, S, d] cache, bf16 or 8-bit codes: box = (box_cols,
+// box_rows, 1 head), swizzled over the box's row where that is 128 or 64 bytes.
+bool make_cache_map(CUtensorMap* map, const void* base, bool codes, long long BH, long long S, int d, int box_cols,
+                    int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
-  const CUtensorMapSwizzle sw = d == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                          : CU_TENSOR_MAP_SWIZZLE_NONE;
+  const int size = codes ? 1 : 2;
+  const CUtensorMapSwizzle sw = box_cols * size == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : box_cols * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                        : CU_TENSOR_MAP_SWIZZLE_NONE;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(BH)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(S) * d};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * size, static_cast<cuuint64_t>(S) * d * size};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -1083,10 +1085,14 @@ int attn_decode_tree(const void* q, const void* k, const void* v, void* o, float
   const size_t need = tree_workspace(plan, d);
   if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
   const long long BH = static_cast<long long>(B) * h_kv;
-  const int box = plan.tc ? 128 : plan.tile / 4;  // a warp's keys, or a whole tile
-  CUtensorMap tq, tk, tv;
-  if (quantised ? (!make_code_map(&tk, k, BH, m, d, box) || !make_code_map(&tv, v, BH, m, d, box))
-                : (!make_tile_map(&tk, k, BH, m, d, box) || !make_tile_map(&tv, v, BH, m, d, box)))
+  // boxes: a warp's keys (mma.sync), a tile, or the halves of a tile that a CTA of
+  // a pair holds (half of K's keys, half of V's columns); bf16 rows of at most 64
+  const int k_rows = plan.tc ? (plan.pair ? 64 : 128) : plan.tile / 4, v_rows = plan.tc ? 128 : k_rows;
+  const int v_d = plan.pair ? d / 2 : d;
+  const int k_cols = quantised || d < 64 ? d : 64, v_cols = quantised || v_d < 64 ? v_d : 64;
+  CUtensorMap tq{}, tk, tv;
+  if (!make_cache_map(&tk, k, quantised, BH, m, d, k_cols, k_rows) ||
+      !make_cache_map(&tv, v, quantised, BH, m, d, v_cols, v_rows))
     return ATTN_ERR_CUDA;
   if (plan.tc && !make_tile_map(&tq, q, BH, rows, d)) return ATTN_ERR_CUDA;
   uint32_t* status = nullptr;

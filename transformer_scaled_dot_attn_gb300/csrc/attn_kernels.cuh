@@ -341,17 +341,18 @@ struct TreeParams {
 // How a step is run: fixed by its sizes and cache type.
 struct TreePlan {
   bool tc;                 // the tcgen05 kernel (128-row query tiles), else mma.sync (16 rows)
+  bool pair;               // ... with two CTAs on 256 rows
   int tile;                // keys of a TMA box
   int row_blocks, block_rows;
   bool by_unit;            // a CTA for each (sequence, key head, row block); no partial results
-  int grid;                // CTAs
+  int grid;                // CTAs (pairs)
   long long slots;         // partial results
 };
 TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised);
 cudaError_t launch_tree(int d, bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
                         const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
 // The tcgen05 kernel (attn_tree_tc.cu).
-cudaError_t launch_tree_tc(int d, bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
-                           const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_tree_tc(int d, bool pair, bool quantised, int grid, int least, const CUtensorMap& tq,
+                           const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
 
 }  // namespace attn

@@ -226,7 +226,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const Watchdog wd = p.wd;
   grid_launch_dependents();
   TreeWalk walk;
-  if (!tree_start(p, C::BN, kTreeLeast, walk)) return;
+  if (!tree_start(p, C::BN, kTreeLeast, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), walk)) return;
   if (tid == 0) {
     for (int w = 0; w < kTreeWarps; ++w)
       for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[w][s], 1);
@@ -737,7 +737,7 @@ template <int D>
 cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
                           const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   cudaError_t e;
-  if (plan.tc) e = launch_tree_tc(D, quantised, plan.grid, kTreeLeastTc, tq, tk, tv, p, stream);
+  if (plan.tc) e = launch_tree_tc(D, plan.pair, quantised, plan.grid, kTreeLeastTc, tq, tk, tv, p, stream);
   else if (quantised) e = launch_small_rows<D, true>(plan.grid, tk, tv, p, stream);
   else e = launch_small_rows<D, false>(plan.grid, tk, tv, p, stream);
   if (e != cudaSuccess || plan.by_unit) return e;
@@ -761,7 +761,8 @@ TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised) {
   TreePlan l{};
   l.tc = tree_uses_tc(rows, d, quantised);
   if (l.tc) {
-    l.block_rows = rows <= 128 ? 128 : 256;
+    l.pair = rows > 128 && d >= 64;
+    l.block_rows = l.pair ? 256 : 128;
     l.tile = 128;
   } else {
     l.block_rows = rows < kTreeRows ? rows : kTreeRows;
@@ -770,9 +771,9 @@ TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised) {
   l.row_blocks = (rows + l.block_rows - 1) / l.block_rows;
   const long long units = static_cast<long long>(B) * h_kv * l.row_blocks;
   const long long tiles = (m + l.tile - 1) / l.tile;
-  const long long room = static_cast<long long>(kSms) * (l.tc ? 1 : small_ctas(d, quantised));
+  const long long room = l.tc ? kSms / (l.pair ? 2 : 1) : kSms * small_ctas(d, quantised);
   // Short caches: a CTA for each unit, nothing to join. Else one CTA for each
-  // place on the GPU's SMs; fewer where the caches hold too few tiles.
+  // place (or pair of places) on the GPU's SMs; fewer where the caches hold too few tiles.
   l.by_unit = tiles <= kTreeShort && (units <= room || (!l.tc && units <= 0x7fffffffLL));
   if (l.by_unit) {
     l.grid = static_cast<int>(units);

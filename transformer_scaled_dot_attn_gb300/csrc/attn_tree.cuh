@@ -52,7 +52,8 @@ __device__ __forceinline__ int tiles_of(int L, int bn) { return L > bn ? (L + bn
 // takes tiles [U c / ctas, U (c + 1) / ctas) of the U on the line: equal shares
 // whatever the lengths, at the price of units that several CTAs hold a part
 // of. The part of unit x that CTA c holds has its place x + c in the partial
-// results (the sum grows from part to part along the line).
+// results (the sum grows from part to part along the line). A pair of CTAs that
+// works as one counts as one here.
 struct TreeLine {
   long long U;
   int ctas;
@@ -100,20 +101,20 @@ struct TreePart {
 };
 
 // Every lane of a warp calls this; false: the CTA has no share.
-__device__ __forceinline__ bool tree_start(const TreeParams& p, int bn, int least, TreeWalk& w) {
+__device__ __forceinline__ bool tree_start(const TreeParams& p, int bn, int least, int cta, int grid, TreeWalk& w) {
   if (p.by_unit) {  // short caches: CTA c takes unit c whole
     const int per_seq = p.h_kv * p.row_blocks;
     w.cta = 0;
-    w.b = static_cast<int>(blockIdx.x) / per_seq;
-    w.idx = static_cast<int>(blockIdx.x) - w.b * per_seq;
+    w.b = cta / per_seq;
+    w.idx = cta - w.b * per_seq;
     w.L = tree_len(p, w.b);
     w.tiles = tiles_of(w.L, bn);
     w.first = w.pos = 0;
     w.end = w.tiles;
     return true;
   }
-  const TreeLine l = tree_line(p, bn, static_cast<int>(gridDim.x), least);
-  w.cta = static_cast<int>(blockIdx.x);
+  const TreeLine l = tree_line(p, bn, grid, least);
+  w.cta = cta;
   if (w.cta >= l.ctas) return false;
   w.pos = l.U * w.cta / l.ctas;
   w.end = l.U * (w.cta + 1) / l.ctas;

@@ -1,20 +1,20 @@
 // Decoding of drafted tokens with many query rows a key head (attn_tree.cu
 // states the operator): tcgen05 tiles of 128 query rows against 128 keys.
 //
-// A CTA holds NQ tiles of 128 rows (one, or two where a key head has more than
-// 128 rows, so that each K/V tile serves 256) and walks its share of the line of
-// tiles (attn_tree.cuh). K and V tiles alternate through one ring of
-// NB 128-key tiles in the tensor cores' layout:
-//   producer    TMA loads. bf16 caches: straight into the ring. e4m3 caches:
-//               the codes into a ring of their own, from which
-//   converters  (4 warps, one key row a thread) write f16 values into the
-//               ring, code 2^(e - top + 7) with `top` the largest scale of the
+// A CTA holds one tile of 128 rows and walks its share of the line of tiles
+// (attn_tree.cuh). Where a key head has more than 128 rows, two CTAs of a cluster
+// work as a pair on 256 (cta_group::2): each holds its 128 rows of Q, S, P and O
+// but only half of every K tile (64 keys) and V tile (half of the columns), so
+// the pair reads, converts and keeps each K/V tile once. The first CTA's issuer
+// feeds both SMs' tensor cores; what it waits for, both CTAs report to it.
+//   producer    TMA loads. bf16 caches: K and V into their rings in the tensor
+//               cores' layout. e4m3 caches: the codes into rings of their own.
+//   converters  (e4m3; 4 warps for K, 4 for V) write f16 values into the K and V
+//               rings, code 2^(e - top + 7) with `top` the largest scale of the
 //               part's keys: so a code is converted once for all rows, one
 //               conversion and one exact product for two codes, and the softmax
 //               carries no scales. f16 holds them exactly down to 2^-22 of the
 //               largest; below that they lose low bits, and 2^-33 becomes 0.
-//               (Exact bf16 values took five operations for two codes: 64 tokens
-//               with eight query heads a key head, d = 128: 119 us.)
 //               The queries are brought to f16 as well, each row to [2^14, 2^15)
 //               by a power of two, and the weights are f16 against a reference
 //               2^7 below the maximum, so that they reach down to 2^-31 of it.
@@ -22,11 +22,19 @@
 //               positions it zeroes the rows past the sequence and values that
 //               are not finite (weight 0 times NaN is NaN). Rows that see such a
 //               value get it added at the end. (The converters do this for e4m3.)
-//   issuer g    S_g = Q_g K^T, O_g += P_g V_g, one thread a query tile.
+//               In a pair it reports Q and K tiles as well.
+//   issuers     one thread for S = Q K^T into one of two S buffers, one for
+//               O += P V: a thread that waits, computes descriptors and commits
+//               between its products takes about as long for a tile's S or P V as
+//               the products themselves (one thread for both: 2900 clocks a tile).
 //   softmax     one thread a row: x = S c, running maximum (O rescaled when it
-//               grew by more than 2^8), p = 2^(x - m), bf16 P over S in TMEM.
-// With NQ = 1 there are two S buffers, so that the next scores are computed
-// during the softmax; with NQ = 2 the other tile's products fill that time.
+//               grew by more than 2^8), p = 2^(x - m), P over S in TMEM, 64 keys
+//               at a time so that their products start while the other 64 are
+//               exponentiated.
+// A waiter must not be overtaken: a wait tells a barrier's phases apart by their
+// parity alone, so every phase that is waited for needs the waiter's own doing
+// before the next one can complete. (So K and V have rings of their own: the
+// cleaner waits for V tiles only.)
 #include "attn_tree.cuh"
 
 #include <atomic>
@@ -39,69 +47,130 @@ using namespace sm103;
 constexpr int kBN = 128;
 constexpr float kGrow = 8.0f;  // log2 units a row maximum may run ahead of its reference
 
-template <int D, int NQ, bool Q8>
+template <int D, bool PAIR, bool Q8>
 struct Tc {
-  static constexpr int ATOM = D >= 64 ? 64 : D;            // bf16 elements of a swizzle row
+  static constexpr int CTAS = PAIR ? 2 : 1;
+  static constexpr int KR = kBN / CTAS;                    // keys of a K tile in this CTA
+  static constexpr int DV = D / CTAS;                      // columns of a V tile in this CTA
+  static constexpr int ATOM = D >= 64 ? 64 : D;            // bf16 elements of a swizzle row (Q, K)
   static constexpr int NATOM = D / ATOM;
   static constexpr uint32_t SWZ = D >= 64 ? 2u : 4u;
   static constexpr uint32_t SBO = 8u * ATOM * 2u;
-  static constexpr uint32_t TILE = kBN * D * 2u;           // a K, V or Q tile in bf16
-  static constexpr uint32_t BOX = kBN * ATOM * 2u;
-  static constexpr uint32_t RAW = Q8 ? kBN * D : 0;        // a tile of codes
-  // Ring of bf16 tiles. For bf16 caches an even number, so that a place always
-  // holds K or always V: the cleaner waits for V tiles only, and a place that K
-  // passes through could complete two phases between its looks (a wait tells
-  // phases apart by their parity alone).
-  static constexpr int NB = Q8 ? (D == 128 ? 3 : 6) : (D == 128 && NQ == 2 ? 4 : 6);
-  static_assert(Q8 || NB % 2 == 0, "the cleaner's waits");
-  static constexpr int NR = Q8 ? (D == 128 ? (NQ == 2 ? 4 : 6) : 8) : 1;     // ring of code tiles
+  static constexpr int ATOMV = DV >= 64 ? 64 : DV;         // the same for V
+  static constexpr int NATOMV = DV / ATOMV;
+  static constexpr uint32_t SWZV = DV >= 64 ? 2u : 4u;
+  static constexpr uint32_t SBOV = 8u * ATOMV * 2u;
+  static constexpr uint32_t QTILE = 128u * D * 2u;
+  static constexpr uint32_t TILE = static_cast<uint32_t>(KR) * D * 2u;   // a K or V tile (the same size)
+  static constexpr uint32_t QBOX = 128u * ATOM * 2u, KBOX = KR * ATOM * 2u, VBOX = kBN * ATOMV * 2u;
+  static constexpr uint32_t RAW = TILE / 2;                // a tile of codes
+  static constexpr int NT = Q8 ? (D == 128 ? (PAIR ? 3 : 2) : 4) : (D == 128 ? (PAIR ? 6 : 3) : 6);  // K ring, V ring
+  static constexpr int NR = Q8 ? (D == 128 ? (PAIR ? 6 : 2) : 4) : 1;                               // code rings
   static constexpr uint32_t OFF_Q = 0;
-  static constexpr uint32_t OFF_B = NQ * TILE;
-  static constexpr uint32_t OFF_R = OFF_B + NB * TILE;
-  static constexpr uint32_t SMEM = OFF_R + (Q8 ? NR * RAW : 0) + 1024;       // + alignment slack
-  static_assert(SMEM <= 227u * 1024u, "shared memory");
-  static constexpr int NS = NQ == 1 ? 2 : 1;               // S buffers of a query tile
-  static constexpr int TM_O = NQ * NS * kBN;               // TMEM: S buffers, then O
-  static constexpr int TMEM = TM_O + NQ * D <= 256 ? 256 : 512;
-  static_assert(TM_O + NQ * D <= 512, "TMEM");
-  static constexpr int SOFT = 4 * NQ;                      // softmax warps
-  static constexpr int PRODUCER = SOFT, ISSUER = SOFT + 1, CLEANER = SOFT + 3;
-  static constexpr int CONV = SOFT + 4;                    // converter warps (e4m3)
-  static constexpr int THREADS = (SOFT + 4 + (Q8 ? 4 : 0)) * 32;
+  static constexpr uint32_t OFF_K = QTILE;
+  static constexpr uint32_t OFF_V = OFF_K + NT * TILE;
+  static constexpr uint32_t OFF_RK = OFF_V + NT * TILE;
+  static constexpr uint32_t OFF_RV = OFF_RK + (Q8 ? NR * RAW : 0);
+  static constexpr uint32_t SMEM = OFF_RV + (Q8 ? NR * RAW : 0) + 1024;  // + alignment slack
+  static_assert(SMEM <= 226u * 1024u, "shared memory");
+  static_assert(DV >= 32, "V's swizzle");
+  static constexpr int TM_O = 2 * kBN;                     // TMEM: two S buffers, then O
+  static constexpr int PRODUCER = 4, ISSUE_S = 5, ISSUE_PV = 6, CLEANER = 7, CONV_K = 8, CONV_V = 12;  // softmax: 0 - 3
+  static constexpr int THREADS = Q8 ? 512 : 256;
+  static constexpr uint32_t FORMAT = Q8 ? (1u << 7) | (1u << 10) : 0u;  // cleared from bf16's descriptor: f16 operands
   // registers: the split must fit in what the CTA is launched with
-  static constexpr bool SPLIT = THREADS > 256;
-  static constexpr int R_LAUNCH = THREADS == 512 ? 128 : 168;
-  static constexpr int R_SOFT = THREADS == 512 ? 184 : 208;
-  static constexpr int R_CTRL = THREADS == 512 ? 48 : 72;
-  static constexpr int R_CONV = !Q8 ? 0 : THREADS == 512 ? 96 : 136;
-  static constexpr int R_SUM = SOFT * 32 * R_SOFT + 128 * R_CTRL + 128 * R_CONV;
-  static_assert(!SPLIT || R_SUM <= R_LAUNCH * THREADS, "register split");
+  static constexpr bool SPLIT = Q8;
+  static constexpr int R_SOFT = 208, R_CTRL = 64, R_CONV = 112;
+  static constexpr int R_SUM = 128 * R_SOFT + 128 * R_CTRL + 256 * R_CONV;
+  static_assert(!SPLIT || R_SUM <= 128 * THREADS, "register split");
 };
 
-constexpr int kMaxRing = 8;
+constexpr int kMaxRing = 6;
 
 struct TcShared {
-  uint64_t q_full, q_empty;
-  uint64_t q_f16[2];                           // e4m3 caches: query tile g is in f16
-  uint64_t scanned;                            // e4m3 caches: the part's scales were looked at
-  uint64_t full[kMaxRing], empty[kMaxRing];    // bf16 tiles: filled (TMA or converters), released by the issuers
-  uint64_t clean[kMaxRing];                    // bf16 caches: the V tile in this place is clean
-  uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];
-  uint64_t s_full[2][2];                       // query tile, S buffer
-  uint64_t p_full[2][2][2];                    // query tile, S buffer, half of the tile's keys
-  uint64_t pv_done[2], o_full[2], o_free[2], drain[2];
-  uint64_t turn[2];                            // two query tiles: their exponentials alternate
+  uint64_t q_full, q_empty;                    // TMA; released by the part's last scores
+  uint64_t q_ready;                            // Q is there (e4m3: in f16) [issuer]
+  uint64_t k_tma[kMaxRing], v_tma[kMaxRing];   // bf16: tile loaded
+  uint64_t k_ready[kMaxRing], v_ready[kMaxRing];  // tile can be multiplied [issuer]
+  uint64_t k_empty[kMaxRing], v_empty[kMaxRing];  // S, P V of the tile complete
+  uint64_t raw_full[2][kMaxRing], raw_empty[2][kMaxRing];  // e4m3: codes of K, V
+  uint64_t scanned[2];                         // e4m3: the part's scales of K, V were looked at
+  uint64_t s_full[2];                          // by S buffer
+  uint64_t p_full[2][2];                       // S buffer, half of the tile's keys [issuer]
+  uint64_t o_free;                             // [issuer]
+  uint64_t drain[2];                           // by issuer
   uint32_t tmem_base;
   int abort_flag;
-  int ref[4][2];                               // e4m3 caches: largest scale byte of K and V, by part
-  int scan[4][4][2];                           // the converter warps' maxima, by part
+  int ref[4][2];                               // e4m3: largest scale byte of K and V, by part
+  int scan[4][2][4];                           // the converter warps' maxima, by part
   int odd[4];                                  // part + 1 whose newest positions hold values that are not finite
 };
 
-// One arrival for the warp, after everything its lanes did before.
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+// ---------------------------------------------------------------- the pair
+
+template <bool PAIR>
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r = 0;
+  if (PAIR) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One arrival for the warp on the issuer's barrier, after everything its lanes did before.
+template <bool PAIR>
+__device__ __forceinline__ void tell_issuer(uint64_t* bar) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  if ((threadIdx.x & 31) != 0) return;
+  // (Release at CTA scope: at cluster scope the arrival took 1200 to 2000 clocks.
+  // What the other SM's thread starts on it, products of this SM's tensor cores,
+  // reads this SM's shared memory and TMEM, whose writes have completed: the
+  // proxy fence or the wait for the TMEM stores came before.)
+  if (PAIR)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_cta(bar, 0)) : "memory");
+  else
+    mbar_arrive(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  if (!PAIR) return mbar_try_wait(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait (see guarded_wait), at cluster scope in a pair.
+template <bool PAIR>
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const Watchdog& wd,
+                                        uint32_t site) {
+  if (!PAIR) return guarded_wait(bar, parity, abort_flag, wd, site);
+  if (try_wait<true>(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!try_wait<true>(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > wd.budget_ns) {
+      *abort_flag = 1;
+      atomicCAS(wd.status, 0u, kDevTimeout | site);
+      return false;
+    }
+  }
+  return true;
 }
 
 // Waits without looking at the abort flag: copies and products in flight must
@@ -117,6 +186,75 @@ __device__ __forceinline__ void tc_drain(uint64_t* bar, uint32_t parity, const W
   }
 }
 
+template <bool PAIR>
+__device__ __forceinline__ void tc_alloc(uint32_t* dst) {
+  if (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc<512>(dst);
+    tmem_relinquish();
+  }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tc_dealloc(uint32_t taddr) {
+  if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+  else tmem_dealloc<512>(taddr);
+}
+
+// A shared-memory descriptor whose start address is moved within its low word.
+struct Desc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+    const uint64_t d = smem_desc(addr, lbo, sbo, swizzle);
+    lo = static_cast<uint32_t>(d);
+    hi = static_cast<uint32_t>(d >> 32);
+  }
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+    return (static_cast<uint64_t>(hi) << 32) | (lo + (bytes >> 4));
+  }
+};
+
+template <bool PAIR>
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    mma_ss(d, a, b, idesc, acc);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    mma_ts(d, a, b, idesc, acc);
+}
+
+// Arrives on *bar (in both CTAs of a pair) when every product issued so far is complete.
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  if (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    mma_commit(bar);
+}
+
+// ---------------------------------------------------------------- layouts and conversions
+
 // O = alpha O in TMEM after a row's reference moved; rare, so out of line.
 template <int NCOL>
 __device__ __noinline__ void tc_rescale(uint32_t t_o, float alpha) {
@@ -131,20 +269,20 @@ __device__ __noinline__ void tc_rescale(uint32_t t_o, float alpha) {
   }
 }
 
-// Byte offset of 16-byte chunk cc of row r in a bf16 tile.
-template <int D>
+// Byte offset of 16-byte chunk cc of row r in a 16-bit tile of COLS columns and ROWS rows.
+template <int COLS, int ROWS>
 __device__ __forceinline__ uint32_t chunk_off(int r, int cc) {
-  constexpr int ATOM = D >= 64 ? 64 : D, CPA = ATOM / 8;
+  constexpr int ATOM = COLS >= 64 ? 64 : COLS, CPA = ATOM / 8;
   const int a = cc / CPA, ca = cc % CPA;
   const int pc = ATOM == 64 ? (ca ^ (r & 7)) : (ca ^ ((r >> 1) & 3));
-  return a * (kBN * ATOM * 2) + r * (ATOM * 2) + (pc << 4);
+  return a * (ROWS * ATOM * 2) + r * (ATOM * 2) + (pc << 4);
 }
 
-// Byte offset of 16-byte chunk cc of row r in a tile of codes.
-template <int D>
+// Byte offset of 16-byte chunk cc of row r in a tile of codes of COLS columns.
+template <int COLS>
 __device__ __forceinline__ uint32_t raw_off(int r, int cc) {
-  const int pc = D == 128 ? (cc ^ (r & 7)) : D == 64 ? (cc ^ ((r >> 1) & 3)) : cc;
-  return r * D + (pc << 4);
+  const int pc = COLS == 128 ? (cc ^ (r & 7)) : COLS == 64 ? (cc ^ ((r >> 1) & 3)) : cc;
+  return r * COLS + (pc << 4);
 }
 
 // Two codes as f16 values times the pair of factors f.
@@ -153,6 +291,12 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t two, uint32_t f) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(f));
   return r;
+}
+
+// 2^e as a pair of f16, e <= 7; below 2^-14 the subnormal numbers that f16 has.
+__device__ __forceinline__ uint32_t pow2_f16x2(int e) {
+  const uint32_t f = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+  return f | (f << 16);
 }
 
 // The larger finite magnitude of a bf16 pair, as bf16 bits (0: none).
@@ -172,7 +316,30 @@ __device__ __forceinline__ uint32_t pack_f16x2_pair(uint64_t v) {
   return pack_f16x2(lo, hi);
 }
 
-// The value (bf16 bits) at column c of a position, for the rare rows that add it themselves.
+// The largest of the bytes [b, e), this thread's share of 128.
+__device__ __forceinline__ int scan_bytes(const unsigned char* b, const unsigned char* e, int t) {
+  const uintptr_t v0 = (reinterpret_cast<uintptr_t>(b) + 15) & ~static_cast<uintptr_t>(15);
+  const uintptr_t v1 = reinterpret_cast<uintptr_t>(e) & ~static_cast<uintptr_t>(15);
+  uint32_t m = 0;
+  if (v0 < v1) {
+    const uint4* v = reinterpret_cast<const uint4*>(v0);
+    const long long count = static_cast<long long>(v1 - v0) / 16;
+#pragma unroll 2
+    for (long long i = t; i < count; i += 128) {
+      const uint4 x = __ldg(v + i);
+      m = __vmaxu4(m, __vmaxu4(__vmaxu4(x.x, x.y), __vmaxu4(x.z, x.w)));
+    }
+    const unsigned char* head = reinterpret_cast<const unsigned char*>(v0);
+    const unsigned char* tail = reinterpret_cast<const unsigned char*>(v1);
+    if (b + t < head) m = __vmaxu4(m, static_cast<uint32_t>(__ldg(b + t)));
+    if (tail + t < e) m = __vmaxu4(m, static_cast<uint32_t>(__ldg(tail + t)));
+  } else {
+    for (const unsigned char* x = b + t; x < e; x += 128) m = __vmaxu4(m, static_cast<uint32_t>(__ldg(x)));
+  }
+  return static_cast<int>(max(max(m & 0xffu, (m >> 8) & 0xffu), max((m >> 16) & 0xffu, m >> 24)));
+}
+
+// The value at column c of a position, for the rare rows that add one that is not finite themselves.
 template <int D, bool Q8>
 __device__ __forceinline__ float value_of(const TreeParams& p, int bh, int key, int c) {
   const size_t row = static_cast<size_t>(bh) * p.m + key;
@@ -185,47 +352,59 @@ __device__ __forceinline__ float value_of(const TreeParams& p, int bh, int key, 
   }
 }
 
-template <int D, int NQ, bool Q8>
-__global__ void __launch_bounds__(Tc<D, NQ, Q8>::THREADS, 1)
+// Reports (to both CTAs of a pair) that part `seg` holds values that are not finite among its newest positions.
+template <bool PAIR>
+__device__ __forceinline__ void mark_odd(TcShared& sh, int seg, uint32_t rank) {
+  *static_cast<volatile int*>(&sh.odd[seg & 3]) = seg + 1;
+  if (PAIR)
+    asm volatile("st.shared::cluster.u32 [%0], %1;\n\tfence.acq_rel.cluster;" ::"r"(
+                     in_cta(&sh.odd[seg & 3], rank ^ 1u)),
+                 "r"(seg + 1)
+                 : "memory");
+}
+
+template <int D, bool PAIR, bool Q8>
+__global__ void __launch_bounds__(Tc<D, PAIR, Q8>::THREADS, 1)
 attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const TreeParams p, int least) {
-  using C = Tc<D, NQ, Q8>;
+  using C = Tc<D, PAIR, Q8>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) TcShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cta_rank<PAIR>();
   volatile int* abort_flag = &sh.abort_flag;
   const Watchdog wd = p.wd;
   grid_launch_dependents();
   TreeWalk walk;
-  if (!tree_start(p, kBN, least, walk)) return;
+  if (!tree_start(p, kBN, least, static_cast<int>(blockIdx.x) / C::CTAS, static_cast<int>(gridDim.x) / C::CTAS, walk))
+    return;  // (both CTAs of a pair, or neither)
   if (tid == 0) {
     mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, NQ);
-    mbar_init(&sh.scanned, 4);
-    for (int s = 0; s < C::NB; ++s) {
-      mbar_init(&sh.full[s], Q8 ? 4 : 1);
-      mbar_init(&sh.empty[s], NQ);
-      mbar_init(&sh.clean[s], 1);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.q_ready, Q8 ? 4 * C::CTAS : C::CTAS);
+    for (int s = 0; s < C::NT; ++s) {
+      mbar_init(&sh.k_tma[s], 1);
+      mbar_init(&sh.v_tma[s], 1);
+      mbar_init(&sh.k_ready[s], Q8 ? 4 * C::CTAS : C::CTAS);
+      mbar_init(&sh.v_ready[s], Q8 ? 4 * C::CTAS : C::CTAS);
+      mbar_init(&sh.k_empty[s], 1);
+      mbar_init(&sh.v_empty[s], 1);
     }
-    for (int s = 0; s < C::NR; ++s) {
-      mbar_init(&sh.raw_full[s], 1);
-      mbar_init(&sh.raw_empty[s], 4);
-    }
-    for (int g = 0; g < NQ; ++g) {
-      mbar_init(&sh.q_f16[g], 4);
-      for (int u = 0; u < 2; ++u) {
-        mbar_init(&sh.s_full[g][u], 1);
-        mbar_init(&sh.p_full[g][u][0], 4);
-        mbar_init(&sh.p_full[g][u][1], 4);
+    for (int u = 0; u < 2; ++u) {
+      for (int s = 0; s < C::NR; ++s) {
+        mbar_init(&sh.raw_full[u][s], 1);
+        mbar_init(&sh.raw_empty[u][s], 4);
       }
-      mbar_init(&sh.pv_done[g], 1);
-      mbar_init(&sh.o_full[g], 1);
-      mbar_init(&sh.o_free[g], 4);
-      mbar_init(&sh.drain[g], 1);
-      mbar_init(&sh.turn[g], 4);
+      mbar_init(&sh.scanned[u], 4);
+      mbar_init(&sh.s_full[u], 1);
+      mbar_init(&sh.p_full[u][0], 4 * C::CTAS);
+      mbar_init(&sh.p_full[u][1], 4 * C::CTAS);
     }
+    mbar_init(&sh.o_free, 4 * C::CTAS);
+    mbar_init(&sh.drain[0], 1);
+    mbar_init(&sh.drain[1], 1);
     sh.abort_flag = 0;
     for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
     fence_mbar_init();
@@ -233,32 +412,33 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  if (warp == C::ISSUER) {
-    tmem_alloc<C::TMEM>(&sh.tmem_base);
-    tmem_relinquish();
-  }
+  if (warp == C::ISSUE_S) tc_alloc<PAIR>(&sh.tmem_base);
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   TreePart part;
   int seg = 0;    // parts done
-  int done = 0;   // tiles done: K tile j of the walk is ring tile 2 j, its V tile 2 j + 1
+  int done = 0;   // tiles done
   bool ok = true;
+  auto wait = [&](uint64_t* bar, int phase, uint32_t site) {
+    return tc_wait<PAIR>(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, wd, site);
+  };
 
-  if (warp < C::SOFT) {
+  if (warp < 4) {
     // ------------------------------------------------------------ softmax, one thread a row
     if (C::SPLIT) reg_alloc<C::R_SOFT>();
-    const int g = warp / 4;
-    const int r = (warp & 3) * 32 + lane;
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_o = tmem + lane_base + C::TM_O + g * D;
+    const int r = tid;
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t t_o = tmem + lane_base + C::TM_O;
     // e4m3: weights against a reference this far below the maximum (log2 units)
     constexpr float kLow = Q8 ? 7.f : 0.f;
 #pragma unroll 1
     while (ok && tree_next(p, kBN, walk, part)) {
       const int old = part.L - p.n;
-      const int row = part.rb * (NQ * 128) + g * 128 + r;
+      const int at = static_cast<int>(rank) * 128 + r;  // row of the block
+      const int row = part.rb * (128 * C::CTAS) + at;
       const bool real = row < p.rows;
       const bool idle = __all_sync(0xffffffffu, !real);  // this warp's rows do not exist
       const unsigned long long word = real ? tree_word(p, part.b, row) : 0ull;
@@ -266,14 +446,14 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       // scale 0: a tiny positive factor keeps -inf (masked) at weight 0
       float c = fmaxf(fabsf(p.c), 1e-30f);
       if constexpr (Q8) {
-        ok = __all_sync(0xffffffffu, guarded_wait(&sh.q_full, seg & 1, abort_flag, wd, kSiteQFull));
+        ok = __all_sync(0xffffffffu, wait(&sh.q_full, seg, kSiteQFull));
         if (!ok) break;
-        uint8_t* tile = smem + C::OFF_Q + g * C::TILE;
+        uint8_t* tile = smem + C::OFF_Q;
         uint4 w[D / 8];
         uint32_t top = 0;
 #pragma unroll
         for (int cc = 0; cc < D / 8; ++cc) {
-          w[cc] = *reinterpret_cast<const uint4*>(tile + chunk_off<D>(r, cc));
+          w[cc] = *reinterpret_cast<const uint4*>(tile + chunk_off<D, 128>(r, cc));
           top = max(top, max(max(finite_top(w[cc].x), finite_top(w[cc].y)), max(finite_top(w[cc].z), finite_top(w[cc].w))));
         }
         const uint32_t up = 268u - max(top >> 7, 15u);
@@ -281,20 +461,18 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         c *= __uint_as_float((254u - up) << 23);
 #pragma unroll
         for (int cc = 0; cc < D / 8; ++cc)
-          *reinterpret_cast<uint4*>(tile + chunk_off<D>(r, cc)) =
+          *reinterpret_cast<uint4*>(tile + chunk_off<D, 128>(r, cc)) =
               make_uint4(to_f16(w[cc].x, f), to_f16(w[cc].y, f), to_f16(w[cc].z, f), to_f16(w[cc].w, f));
         fence_proxy_async_smem();
-        warp_arrive(&sh.q_f16[g]);
+        tell_issuer<PAIR>(&sh.q_ready);
       }
       float m_used = -INFINITY, l = 0.f;
       uint64_t c2 = f2_pack(c, c);
 #pragma unroll 1
       for (int j = 0; j < T; ++j) {
-        const int gi = done + j;
-        const int u = C::NS == 2 ? (gi & 1) : 0;
-        const uint32_t ph = (C::NS == 2 ? gi >> 1 : gi) & 1;
-        const uint32_t t_s = tmem + lane_base + (g * C::NS + u) * kBN;
-        ok = __all_sync(0xffffffffu, guarded_wait(&sh.s_full[g][u], ph, abort_flag, wd, kSiteSFull));
+        const int gi = done + j, u = gi & 1;
+        const uint32_t t_s = tmem + lane_base + u * kBN;
+        ok = __all_sync(0xffffffffu, wait(&sh.s_full[u], gi >> 1, kSiteSFull));
         if (!ok) break;
         tc_fence_after();
         if (Q8 && j == 0) {  // the part's largest K scale is known by now
@@ -302,10 +480,9 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           c2 = f2_pack(c, c);
         }
         if (idle) {
-          if (NQ == 2) warp_arrive(&sh.turn[g ^ 1]);
           tc_fence_before();
-          warp_arrive(&sh.p_full[g][u][0]);
-          warp_arrive(&sh.p_full[g][u][1]);
+          tell_issuer<PAIR>(&sh.p_full[u][0]);
+          tell_issuer<PAIR>(&sh.p_full[u][1]);
           continue;
         }
         uint32_t s[4][32];
@@ -344,15 +521,9 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         const float m_ref = m_used == -INFINITY ? 0.f : m_used - kLow;  // nothing seen yet: weights 0
         const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
-        if (NQ == 2 && (g == 1 || gi > 0)) {
-          // the exponentials of the two query tiles take turns (0, 1, 0, 1, ...), so
-          // that one tile's overlap the other's products
-          ok = __all_sync(0xffffffffu, guarded_wait(&sh.turn[g], (g == 1 ? gi : gi - 1) & 1, abort_flag, wd, kSiteExpTurn));
-          if (!ok) break;
-        }
         if (j > 0 && __any_sync(0xffffffffu, moved)) {
-          // the products so far are in O (with two S buffers the scores do not show that)
-          ok = __all_sync(0xffffffffu, guarded_wait(&sh.pv_done[g], (gi - 1) & 1, abort_flag, wd, kSitePFull));
+          // the products so far are in O (the scores, a buffer ahead, do not show that)
+          ok = __all_sync(0xffffffffu, wait(&sh.v_empty[(gi - 1) % C::NT], (gi - 1) / C::NT, kSitePFull));
           if (!ok) break;
           tc_fence_after();
           tc_rescale<D>(t_o, alpha);
@@ -378,18 +549,18 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             tmem_st16(t_s + q * 16, pk);
           }
-          if (NQ == 2 && half == 1) warp_arrive(&sh.turn[g ^ 1]);
           tmem_st_wait();
           tc_fence_before();
-          warp_arrive(&sh.p_full[g][u][half]);
+          tell_issuer<PAIR>(&sh.p_full[u][half]);
         }
         float a0, a1, a2, a3;
         f2_unpack(acc0, a0, a1);
         f2_unpack(acc1, a2, a3);
         l = (a0 + a1) + (a2 + a3);
       }
-      if (ok)
-        ok = __all_sync(0xffffffffu, guarded_wait(&sh.o_full[g], seg & 1, abort_flag, wd, kSiteOFull));
+      // the last tile's product
+      done += T;
+      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.v_empty[(done - 1) % C::NT], (done - 1) / C::NT, kSiteOFull));
       if (!ok) break;
       tc_fence_after();
       if (!idle) {
@@ -399,7 +570,6 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         m_used = m_used == -INFINITY ? (l != 0.f ? 0.f : -INFINITY) : m_used - kLow;
         const float inv = m_used == -INFINITY ? 0.f : unit_v / l;
         const size_t out = static_cast<size_t>(part.bh) * p.rows + row;
-        const int at = g * 128 + r;  // row of the block
         // (not unrolled: each turn's loads and stores are independent of the others')
 #pragma unroll 1
         for (int q = 0; q < D / 16; ++q) {
@@ -446,115 +616,100 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
       }
       tc_fence_before();
-      warp_arrive(&sh.o_free[g]);
-      done += T;
+      tell_issuer<PAIR>(&sh.o_free);
       ++seg;
     }
-  } else if (Q8 && warp >= C::CONV) {
-    // ------------------------------------------------------------ converters, one key row a thread
+  } else if (Q8 && warp >= C::CONV_K) {
+    // ------------------------------------------------------------ converters
     if (C::SPLIT) reg_dealloc<C::R_CONV>();
-    const int r = tid - C::CONV * 32;
+    const bool is_v = warp >= C::CONV_V;
+    const int t = tid - (is_v ? C::CONV_V : C::CONV_K) * 32, wi = t >> 5;
+    // a thread converts one row of V, or of K (pair: one of the halves of a row)
+    const int r = is_v ? t : t % C::KR;
+    const int c0 = is_v ? 0 : t / C::KR * (C::DV / 16);  // first 16-byte chunk
+    const unsigned char* exps = is_v ? p.v_exp : p.k_exp;
+    uint8_t* ring = smem + (is_v ? C::OFF_V : C::OFF_K);
+    const uint8_t* raw = smem + (is_v ? C::OFF_RV : C::OFF_RK);
+    uint64_t* ready = is_v ? sh.v_ready : sh.k_ready;
+    uint64_t* empty = is_v ? sh.v_empty : sh.k_empty;
 #pragma unroll 1
     while (ok && tree_next(p, kBN, walk, part)) {
       const int old = part.L - p.n, T = part.t1 - part.t0;
-      const size_t row0 = static_cast<size_t>(part.bh) * p.m;
+      const unsigned char* row = exps + static_cast<size_t>(part.bh) * p.m;
       const int key_end = min(part.L, part.t1 * kBN);
-      // the largest scales of the part's keys
-      int top[2] = {0, 0};
-#pragma unroll 4
-      for (int key = part.t0 * kBN + r; key < key_end; key += kBN) {
-        top[0] = max(top[0], static_cast<int>(__ldg(p.k_exp + row0 + key)));
-        top[1] = max(top[1], static_cast<int>(__ldg(p.v_exp + row0 + key)));
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        top[u] = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top[u])));
-        if (lane == 0) sh.scan[seg & 3][warp - C::CONV][u] = top[u];
-      }
+      // the largest scale of the part's keys
+      int top = scan_bytes(row + min(part.t0 * kBN, key_end), row + key_end, t);
+      top = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top)));
+      if (lane == 0) sh.scan[seg & 3][is_v][wi] = top;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.scanned);
-      ok = __all_sync(0xffffffffu, guarded_wait(&sh.scanned, seg & 1, abort_flag, wd, kSiteKFull));
+      if (lane == 0) mbar_arrive(&sh.scanned[is_v]);
+      ok = __all_sync(0xffffffffu, guarded_wait(&sh.scanned[is_v], seg & 1, abort_flag, wd, kSiteKFull));
       if (!ok) break;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int* of = &sh.scan[seg & 3][0][u];
-        top[u] = max(max(of[0], of[2]), max(of[4], of[6]));
-        if (r == 0) sh.ref[seg & 3][u] = top[u];
-      }
-      int bytes[2] = {0, 0};
-      auto scales = [&](int j) {  // of the tile's K and V row, read a tile ahead
-        const int key = (part.t0 + j) * kBN + r;
-        if (key < key_end) {
-          bytes[0] = __ldg(p.k_exp + row0 + key);
-          bytes[1] = __ldg(p.v_exp + row0 + key);
-        }
-      };
-      scales(0);
+      const int* of = sh.scan[seg & 3][is_v];
+      top = max(max(of[0], of[1]), max(of[2], of[3]));
+      if (t == 0) sh.ref[seg & 3][is_v] = top;
+      const int first = part.t0 * kBN + (is_v ? 0 : static_cast<int>(rank) * C::KR) + r;  // this thread's key of a tile
+      int byte = first < key_end ? __ldg(row + first) : 0;  // read a tile ahead
 #pragma unroll 1
-      for (int j = 0; ok && j < T; ++j) {
-        // 2^(e - top + 7) in f16, below 2^-14 as the subnormal numbers it has
-        uint32_t f2[2];
+      for (int j = 0; j < T; ++j) {
+        const uint32_t f = pow2_f16x2(byte - top + 7);
+        const int key = first + j * kBN;
+        if (key + kBN < key_end) byte = __ldg(row + key + kBN);
+        const int gi = done + j, rs = gi % C::NR, bs = gi % C::NT;
+        ok = guarded_wait(&sh.raw_full[is_v][rs], (gi / C::NR) & 1, abort_flag, wd, kSiteKFull) &&
+             (gi < C::NT || wait(&empty[bs], gi / C::NT - 1, kSiteKEmpty));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t* src = raw + rs * C::RAW;
+        uint8_t* dst = ring + bs * C::TILE;
+        if (!is_v) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int e = bytes[u] - top[u] + 7;
-          const uint32_t f = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
-          f2[u] = f | (f << 16);
-        }
-        scales(j + 1);
-        const int key = (part.t0 + j) * kBN + r;
-        const bool tail = (part.t0 + j + 1) * kBN > old;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const int h = 2 * (done + j) + kv;
-          const int rs = h % C::NR, bs = h % C::NB;
-          ok = guarded_wait(&sh.raw_full[rs], (h / C::NR) & 1, abort_flag, wd, kSiteKFull) &&
-               (h < C::NB || guarded_wait(&sh.empty[bs], (h / C::NB - 1) & 1, abort_flag, wd, kSiteKEmpty));
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint8_t* src = smem + C::OFF_R + rs * C::RAW;
-          uint8_t* dst = smem + C::OFF_B + bs * C::TILE;
-          const uint32_t f = f2[kv];
-          if (kv == 1 && tail) {
-            // Rows past the sequence are anyone's: zeros. NaN codes become zeros
-            // too (a weight of 0 would make them NaN for rows that do not see
-            // them); the rows that do see them add them at the end.
-            const bool zero = key >= part.L;
-            bool odd = false;
-            for (int cc = 0; cc < D / 16; ++cc) {
-              const uint4 w4 = *reinterpret_cast<const uint4*>(src + raw_off<D>(r, cc));
-              uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-              uint32_t o[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t n = nan_codes(w[i]) & 0x80808080u;
-                odd |= n != 0;
-                w[i] = zero ? 0u : w[i] & ~((n >> 7) * 0xffu);
-                o[2 * i] = codes_f16(w[i] & 0xffffu, f);
-                o[2 * i + 1] = codes_f16(w[i] >> 16, f);
-              }
-              *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            if (odd && !zero) sh.odd[seg & 3] = seg + 1;
-          } else {
-#pragma unroll
-            for (int cc = 0; cc < D / 16; ++cc) {
-              const uint4 w = *reinterpret_cast<const uint4*>(src + raw_off<D>(r, cc));
-              *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc)) =
-                  make_uint4(codes_f16(w.x & 0xffffu, f), codes_f16(w.x >> 16, f), codes_f16(w.y & 0xffffu, f),
-                             codes_f16(w.y >> 16, f));
-              *reinterpret_cast<uint4*>(dst + chunk_off<D>(r, 2 * cc + 1)) =
-                  make_uint4(codes_f16(w.z & 0xffffu, f), codes_f16(w.z >> 16, f), codes_f16(w.w & 0xffffu, f),
-                             codes_f16(w.w >> 16, f));
-            }
+          for (int cc = 0; cc < C::DV / 16; ++cc) {
+            const uint4 w = *reinterpret_cast<const uint4*>(src + raw_off<D>(r, c0 + cc));
+            *reinterpret_cast<uint4*>(dst + chunk_off<D, C::KR>(r, 2 * (c0 + cc))) =
+                make_uint4(codes_f16(w.x & 0xffffu, f), codes_f16(w.x >> 16, f), codes_f16(w.y & 0xffffu, f),
+                           codes_f16(w.y >> 16, f));
+            *reinterpret_cast<uint4*>(dst + chunk_off<D, C::KR>(r, 2 * (c0 + cc) + 1)) =
+                make_uint4(codes_f16(w.z & 0xffffu, f), codes_f16(w.z >> 16, f), codes_f16(w.w & 0xffffu, f),
+                           codes_f16(w.w >> 16, f));
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sh.full[bs]);
-            mbar_arrive(&sh.raw_empty[rs]);
+        } else if ((part.t0 + j + 1) * kBN <= old) {
+#pragma unroll
+          for (int cc = 0; cc < C::DV / 16; ++cc) {
+            const uint4 w = *reinterpret_cast<const uint4*>(src + raw_off<C::DV>(r, cc));
+            *reinterpret_cast<uint4*>(dst + chunk_off<C::DV, kBN>(r, 2 * cc)) =
+                make_uint4(codes_f16(w.x & 0xffffu, f), codes_f16(w.x >> 16, f), codes_f16(w.y & 0xffffu, f),
+                           codes_f16(w.y >> 16, f));
+            *reinterpret_cast<uint4*>(dst + chunk_off<C::DV, kBN>(r, 2 * cc + 1)) =
+                make_uint4(codes_f16(w.z & 0xffffu, f), codes_f16(w.z >> 16, f), codes_f16(w.w & 0xffffu, f),
+                           codes_f16(w.w >> 16, f));
           }
+        } else {
+          // Rows past the sequence are anyone's: zeros. NaN codes become zeros
+          // too (a weight of 0 would make them NaN for rows that do not see
+          // them); the rows that do see them add them at the end.
+          const bool zero = key >= part.L;
+          bool odd = false;
+          for (int cc = 0; cc < C::DV / 16; ++cc) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(src + raw_off<C::DV>(r, cc));
+            uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t n = nan_codes(w[i]) & 0x80808080u;
+              odd |= n != 0;
+              w[i] = zero ? 0u : w[i] & ~((n >> 7) * 0xffu);
+              o[2 * i] = codes_f16(w[i] & 0xffffu, f);
+              o[2 * i + 1] = codes_f16(w[i] >> 16, f);
+            }
+            *reinterpret_cast<uint4*>(dst + chunk_off<C::DV, kBN>(r, 2 * cc)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + chunk_off<C::DV, kBN>(r, 2 * cc + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          if (odd && !zero) mark_odd<PAIR>(sh, seg, rank);
         }
+        fence_proxy_async_smem();
+        tell_issuer<PAIR>(&ready[bs]);
+        if (lane == 0) mbar_arrive(&sh.raw_empty[is_v][rs]);
       }
       done += T;
       ++seg;
@@ -564,134 +719,163 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (warp == C::PRODUCER) {
       // ---------------------------------------------------------- TMA producer
       if (lane == 0) {
-        constexpr int N = Q8 ? C::NR : C::NB;
-        uint64_t* fulls = Q8 ? sh.raw_full : sh.full;
-        uint64_t* empties = Q8 ? sh.raw_empty : sh.empty;
-        int loaded = 0;  // ring tiles put on their way
-        int q_parts = 0;
+        constexpr int N = Q8 ? C::NR : C::NT;
+        constexpr uint32_t BYTES = Q8 ? C::RAW : C::TILE;
+        uint64_t* kf = Q8 ? sh.raw_full[0] : sh.k_tma;
+        uint64_t* vf = Q8 ? sh.raw_full[1] : sh.v_tma;
+        uint64_t* ke = Q8 ? sh.raw_empty[0] : sh.k_empty;
+        uint64_t* ve = Q8 ? sh.raw_empty[1] : sh.v_empty;
+        uint8_t* kd = smem + (Q8 ? C::OFF_RK : C::OFF_K);
+        uint8_t* vd = smem + (Q8 ? C::OFF_RV : C::OFF_V);
+        int k_loaded = 0, v_loaded = 0, q_loaded = 0;
 #pragma unroll 1
         while (ok && tree_next(p, kBN, walk, part)) {
           const int T = part.t1 - part.t0;
-          if (seg > 0) ok = guarded_wait(&sh.q_empty, (seg - 1) & 1, abort_flag, wd, kSiteQFull);
+          if (seg > 0) ok = wait(&sh.q_empty, seg - 1, kSiteQFull);
           if (!ok) break;
-          const int q0 = part.rb * (NQ * 128);
-          mbar_arrive_expect_tx(&sh.q_full, NQ * C::TILE);
-          ++q_parts;
-          for (int t = 0; t < NQ; ++t)  // (rows past the last load as zeros)
-            for (int a = 0; a < C::NATOM; ++a)
-              tma_load_3d(smem + C::OFF_Q + t * C::TILE + a * C::BOX, &tm_q, &sh.q_full, a * C::ATOM,
-                          q0 + t * 128, part.bh);
-          for (int x = 0; ok && x < 2 * T; ++x) {
-            const int h = 2 * done + x, st = h % N;
-            if (h >= N) ok = guarded_wait(&empties[st], (h / N - 1) & 1, abort_flag, wd, kSiteKEmpty);
+          const int q0 = part.rb * (128 * C::CTAS) + static_cast<int>(rank) * 128;
+          mbar_arrive_expect_tx(&sh.q_full, C::QTILE);
+          ++q_loaded;
+          for (int a = 0; a < C::NATOM; ++a)  // (rows past the last load as zeros)
+            tma_load_3d(smem + C::OFF_Q + a * C::QBOX, &tm_q, &sh.q_full, a * C::ATOM, q0, part.bh);
+          for (int j = 0; ok && j < T; ++j) {
+            const int gi = done + j, st = gi % N;
+            const int k0 = (part.t0 + j) * kBN;
+            const int kk = k0 + static_cast<int>(rank) * C::KR, vc = static_cast<int>(rank) * C::DV;
+            if (gi >= N) ok = wait(&ke[st], gi / N - 1, kSiteKEmpty);
             if (!ok) break;
-            const CUtensorMap* map = (x & 1) ? &tm_v : &tm_k;
-            const int k0 = (part.t0 + x / 2) * kBN;
+            mbar_arrive_expect_tx(&kf[st], BYTES);
             if (Q8) {
-              mbar_arrive_expect_tx(&fulls[st], C::RAW);
-              tma_load_3d(smem + C::OFF_R + st * C::RAW, map, &fulls[st], 0, k0, part.bh);
+              tma_load_3d(kd + st * BYTES, &tm_k, &kf[st], 0, kk, part.bh);
             } else {
-              mbar_arrive_expect_tx(&fulls[st], C::TILE);
               for (int a = 0; a < C::NATOM; ++a)
-                tma_load_3d(smem + C::OFF_B + st * C::TILE + a * C::BOX, map, &fulls[st], a * C::ATOM, k0, part.bh);
+                tma_load_3d(kd + st * BYTES + a * C::KBOX, &tm_k, &kf[st], a * C::ATOM, kk, part.bh);
             }
-            ++loaded;
+            ++k_loaded;
+            if (gi >= N) ok = wait(&ve[st], gi / N - 1, kSiteVEmpty);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&vf[st], BYTES);
+            if (Q8) {
+              tma_load_3d(vd + st * BYTES, &tm_v, &vf[st], vc, k0, part.bh);
+            } else {
+              for (int a = 0; a < C::NATOMV; ++a)
+                tma_load_3d(vd + st * BYTES + a * C::VBOX, &tm_v, &vf[st], vc + a * C::ATOMV, k0, part.bh);
+            }
+            ++v_loaded;
           }
           done += T;
           ++seg;
         }
         // every copy lands before shared memory is released
-        if (q_parts > 0) tc_drain(&sh.q_full, (q_parts - 1) & 1, wd);
-        for (int x = max(0, loaded - N); x < loaded; ++x) tc_drain(&fulls[x % N], (x / N) & 1, wd);
+        if (q_loaded > 0) tc_drain(&sh.q_full, (q_loaded - 1) & 1, wd);
+        for (int x = max(0, k_loaded - N); x < k_loaded; ++x) tc_drain(&kf[x % N], (x / N) & 1, wd);
+        for (int x = max(0, v_loaded - N); x < v_loaded; ++x) tc_drain(&vf[x % N], (x / N) & 1, wd);
       }
-    } else if (warp < C::ISSUER + NQ) {
-      // ---------------------------------------------------------- issuer of query tile g
-      const int g = warp - C::ISSUER;
-      if (lane == 0) {
-        constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);  // operand formats of the descriptor; f16 is 0
-        const uint32_t idesc_s =
-            (idesc_bf16_f32(128, kBN, false, false) & ~(Q8 ? kBf16 : 0u)) | (p.c < 0.f ? (1u << 13) : 0u);
-        const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true) & ~(Q8 ? kBf16 : 0u);
-        const uint32_t sq = smem_u32(smem + C::OFF_Q) + g * C::TILE;
-        const uint32_t sb = smem_u32(smem + C::OFF_B);
-        const uint32_t t_s = tmem + g * C::NS * kBN, t_o = tmem + C::TM_O + g * D;
-        auto k_ready = [&](int gi) {
-          const int h = 2 * gi;
-          return guarded_wait(&sh.full[h % C::NB], (h / C::NB) & 1, abort_flag, wd, kSiteKFull);
-        };
-        auto scores = [&](int gi) {  // S of the walk's tile gi, whose K tile is there
-          const int st = 2 * gi % C::NB, u = C::NS == 2 ? (gi & 1) : 0;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const int a = k / (C::ATOM / 16), w = k % (C::ATOM / 16);
-            mma_ss(t_s + u * kBN, smem_desc(sq + a * C::BOX + w * 32, 16, C::SBO, C::SWZ),
-                   smem_desc(sb + st * C::TILE + a * C::BOX + w * 32, 16, C::SBO, C::SWZ), idesc_s, k > 0 ? 1u : 0u);
-          }
-          mma_commit(&sh.s_full[g][u]);
-          mma_commit(&sh.empty[st]);
-        };
+    } else if (warp == C::ISSUE_S) {
+      // ---------------------------------------------------------- S (the pair's first CTA)
+      if (rank == 0 && lane == 0) {
+        const uint32_t idesc =
+            (idesc_bf16_f32(128 * C::CTAS, kBN, false, false) & ~C::FORMAT) | (p.c < 0.f ? (1u << 13) : 0u);
+        const Desc dq(smem_u32(smem + C::OFF_Q), 16, C::SBO, C::SWZ), dk(smem_u32(smem + C::OFF_K), 16, C::SBO, C::SWZ);
+        uint64_t* kr = (Q8 || PAIR) ? sh.k_ready : sh.k_tma;
+        uint64_t* qr = (Q8 || PAIR) ? &sh.q_ready : &sh.q_full;
 #pragma unroll 1
         while (ok && tree_next(p, kBN, walk, part)) {
           const int T = part.t1 - part.t0;
-          ok = guarded_wait(Q8 ? &sh.q_f16[g] : &sh.q_full, seg & 1, abort_flag, wd, kSiteQFull) && k_ready(done);
-          if (ok) scores(done);
+          ok = wait(qr, seg, kSiteQFull);
+#pragma unroll 1
           for (int j = 0; ok && j < T; ++j) {
-            const int gi = done + j, h = 2 * gi + 1, st = h % C::NB;
-            const int u = C::NS == 2 ? (gi & 1) : 0;
-            const uint32_t ph = (C::NS == 2 ? gi >> 1 : gi) & 1;
-            if (C::NS == 2 && j + 1 < T) {
-              if (!(ok = k_ready(gi + 1))) break;
-              scores(gi + 1);
-            }
-            if (j + 1 == T) mma_commit(&sh.q_empty);  // this part's last scores are on their way
-            // what is there long before the weights is waited for first
-            ok = guarded_wait(Q8 ? &sh.full[st] : &sh.clean[st], (h / C::NB) & 1, abort_flag, wd, kSiteVFull);
-            if (ok && C::NS == 1 && j + 1 < T) ok = k_ready(gi + 1);
-            // the previous part's O has been read
-            if (ok && j == 0 && seg > 0) ok = guarded_wait(&sh.o_free[g], (seg - 1) & 1, abort_flag, wd, kSiteOFull);
-            for (int half = 0; ok && half < 2; ++half) {
-              if (!(ok = guarded_wait(&sh.p_full[g][u][half], ph, abort_flag, wd, kSitePFull))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < kBN / 32; ++k)
-                mma_ts(t_o, t_s + u * kBN + half * 32 + k * 8,
-                       smem_desc(sb + st * C::TILE + (half * 4 + k) * 16 * C::ATOM * 2, C::BOX, C::SBO, C::SWZ), idesc_o,
-                       (j > 0 || half > 0 || k > 0) ? 1u : 0u);
-            }
+            const int gi = done + j, st = gi % C::NT, u = gi & 1;
+            ok = wait(&kr[st], gi / C::NT, kSiteKFull);
+            // the buffer's weights have been multiplied
+            if (ok && gi >= 2) ok = wait(&sh.v_empty[(gi - 2) % C::NT], (gi - 2) / C::NT, kSiteSFull);
             if (!ok) break;
-            mma_commit(&sh.empty[st]);
-            mma_commit(&sh.pv_done[g]);
-            if (j + 1 == T) mma_commit(&sh.o_full[g]);
-            if (C::NS == 1 && j + 1 < T) scores(gi + 1);
+            tc_fence_after();
+            const uint32_t at = st * C::TILE;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const int a = k / (C::ATOM / 16), w = k % (C::ATOM / 16);
+              tc_mma_ss<PAIR>(tmem + u * kBN, dq.at(a * C::QBOX + w * 32), dk.at(at + a * C::KBOX + w * 32), idesc,
+                              k > 0 ? 1u : 0u);
+            }
+            tc_commit<PAIR>(&sh.s_full[u]);
+            tc_commit<PAIR>(&sh.k_empty[st]);
           }
+          if (ok) tc_commit<PAIR>(&sh.q_empty);  // the part's last scores
           done += T;
           ++seg;
         }
         // every product finishes before TMEM is released
-        mma_commit(&sh.drain[g]);
-        tc_drain(&sh.drain[g], 0, wd);
+        tc_commit<PAIR>(&sh.drain[0]);
+        tc_drain(&sh.drain[0], 0, wd);
       }
+      // (the second CTA: the last of the arrivals that reach into it)
+      if (PAIR && rank == 1 && lane == 0) tc_drain(&sh.drain[0], 0, wd);
+      __syncwarp();
+    } else if (warp == C::ISSUE_PV) {
+      // ---------------------------------------------------------- P V (the pair's first CTA)
+      if (rank == 0 && lane == 0) {
+        const uint32_t idesc = idesc_bf16_f32(128 * C::CTAS, D, false, true) & ~C::FORMAT;
+        const Desc dv(smem_u32(smem + C::OFF_V), C::VBOX, C::SBOV, C::SWZV);
+        const uint32_t t_o = tmem + C::TM_O;
+#pragma unroll 1
+        while (ok && tree_next(p, kBN, walk, part)) {
+          const int T = part.t1 - part.t0;
+          if (seg > 0) ok = wait(&sh.o_free, seg - 1, kSiteOFull);  // the previous part's O has been read
+#pragma unroll 1
+          for (int j = 0; ok && j < T; ++j) {
+            const int gi = done + j, st = gi % C::NT, u = gi & 1;
+            ok = wait(&sh.v_ready[st], gi / C::NT, kSiteVFull);
+            const uint32_t at = st * C::TILE;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (ok) ok = wait(&sh.p_full[u][half], gi >> 1, kSitePFull);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < kBN / 32; ++k)
+                tc_mma_ts<PAIR>(t_o, tmem + u * kBN + half * 32 + k * 8,
+                                dv.at(at + (half * 4 + k) * 16 * C::ATOMV * 2), idesc,
+                                (j > 0 || half > 0 || k > 0) ? 1u : 0u);
+            }
+            if (ok) tc_commit<PAIR>(&sh.v_empty[st]);
+          }
+          done += T;
+          ++seg;
+        }
+        tc_commit<PAIR>(&sh.drain[1]);
+        tc_drain(&sh.drain[1], 0, wd);
+      }
+      if (PAIR && rank == 1 && lane == 0) tc_drain(&sh.drain[1], 0, wd);
       __syncwarp();
     } else if (!Q8 && warp == C::CLEANER) {
       // ---------------------------------------------------------- cleaner of V tiles
 #pragma unroll 1
       while (ok && tree_next(p, kBN, walk, part)) {
         const int old = part.L - p.n, T = part.t1 - part.t0;
+        if (PAIR) {
+          ok = __all_sync(0xffffffffu, wait(&sh.q_full, seg, kSiteQFull));
+          if (!ok) break;
+          tell_issuer<PAIR>(&sh.q_ready);
+        }
 #pragma unroll 1
-        for (int j = 0; ok && j < T; ++j) {
-          const int h = 2 * (done + j) + 1, st = h % C::NB;
-          ok = guarded_wait(&sh.full[st], (h / C::NB) & 1, abort_flag, wd, kSiteVFull);
-          ok = __all_sync(0xffffffffu, ok);
+        for (int j = 0; j < T; ++j) {
+          const int gi = done + j, st = gi % C::NT;
+          if (PAIR) {
+            ok = __all_sync(0xffffffffu, wait(&sh.k_tma[st], gi / C::NT, kSiteKFull));
+            if (!ok) break;
+            tell_issuer<PAIR>(&sh.k_ready[st]);
+          }
+          ok = __all_sync(0xffffffffu, wait(&sh.v_tma[st], gi / C::NT, kSiteVFull));
           if (!ok) break;
           const int k0 = (part.t0 + j) * kBN;
           if (k0 + kBN > old) {
             bool odd = false;
-            uint8_t* tile = smem + C::OFF_B + st * C::TILE;
-            for (int x = lane; x < kBN * (D / 8); x += 32) {
-              const int r = x / (D / 8);
-              uint4* at = reinterpret_cast<uint4*>(tile + chunk_off<D>(r, x % (D / 8)));
-              uint4 v = *at;
+            uint8_t* tile = smem + C::OFF_V + st * C::TILE;
+            for (int x = lane; x < kBN * (C::DV / 8); x += 32) {
+              const int r = x / (C::DV / 8);
+              uint4* cell = reinterpret_cast<uint4*>(tile + chunk_off<C::DV, kBN>(r, x % (C::DV / 8)));
+              uint4 v = *cell;
               uint32_t* w = reinterpret_cast<uint32_t*>(&v);
               bool dirty = false;
 #pragma unroll
@@ -702,13 +886,12 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 dirty |= y != w[i];
                 w[i] = y;
               }
-              if (dirty) *at = v;
+              if (dirty) *cell = v;
             }
-            if (odd) sh.odd[seg & 3] = seg + 1;
+            if (odd) mark_odd<PAIR>(sh, seg, rank);
             fence_proxy_async_smem();
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.clean[st]);
+          tell_issuer<PAIR>(&sh.v_ready[st]);
         }
         done += T;
         ++seg;
@@ -718,23 +901,24 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == C::ISSUER) {
+  if (PAIR) cluster_sync();  // nothing reaches into the other CTA any more
+  if (warp == C::ISSUE_S) {
     tc_fence_after();
-    tmem_dealloc<C::TMEM>(tmem);
+    tc_dealloc<PAIR>(tmem);
   }
 }
 
-template <int D, int NQ, bool Q8>
+template <int D, bool PAIR, bool Q8>
 cudaError_t launch_tc(int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const TreeParams& p, cudaStream_t stream) {
-  using C = Tc<D, NQ, Q8>;
+  using C = Tc<D, PAIR, Q8>;
   static std::atomic<int> ready[64];  // 1: usable, 2: the register split does not fit the compiled kernel
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   int state = ready[dev & 63].load(std::memory_order_relaxed);
   if (state == 0) {
-    e = cudaFuncSetAttribute(attn_tree_tc_kernel<D, NQ, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_tree_tc_kernel<D, PAIR, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
     state = 1;
@@ -742,39 +926,49 @@ cudaError_t launch_tc(int grid, int least, const CUtensorMap& tq, const CUtensor
       // setmaxnreg.inc waits until registers are free: the shares must fit in
       // what the CTA is launched with, or the kernel would never proceed
       cudaFuncAttributes fa;
-      if ((e = cudaFuncGetAttributes(&fa, attn_tree_tc_kernel<D, NQ, Q8>)) != cudaSuccess) return e;
+      if ((e = cudaFuncGetAttributes(&fa, attn_tree_tc_kernel<D, PAIR, Q8>)) != cudaSuccess) return e;
       if (fa.numRegs * C::THREADS < C::R_SUM) state = 2;
     }
     ready[dev & 63].store(state, std::memory_order_relaxed);
   }
   if (state == 2) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = C::CTAS;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * C::CTAS));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
   prof_begin(kKindTree, stream);
-  attn_tree_tc_kernel<D, NQ, Q8><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM, stream>>>(tq, tk, tv, p, least);
-  e = cudaGetLastError();
+  e = cudaLaunchKernelEx(&cfg, attn_tree_tc_kernel<D, PAIR, Q8>, tq, tk, tv, p, least);
   prof_end(kKindTree, stream);
   return e;
 }
 
-template <int D>
-cudaError_t launch_tc_d(bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
-                        const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
-  if (p.block_rows == 128)
-    return quantised ? launch_tc<D, 1, true>(grid, least, tq, tk, tv, p, stream)
-                     : launch_tc<D, 1, false>(grid, least, tq, tk, tv, p, stream);
-  return quantised ? launch_tc<D, 2, true>(grid, least, tq, tk, tv, p, stream)
-                   : launch_tc<D, 2, false>(grid, least, tq, tk, tv, p, stream);
-}
-
 }  // namespace
 
-cudaError_t launch_tree_tc(int d, bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
-                           const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
-  switch (d) {
-    case 32: return launch_tc_d<32>(quantised, grid, least, tq, tk, tv, p, stream);
-    case 64: return launch_tc_d<64>(quantised, grid, least, tq, tk, tv, p, stream);
-    case 128: return launch_tc_d<128>(quantised, grid, least, tq, tk, tv, p, stream);
-    default: return cudaErrorInvalidValue;
-  }
+cudaError_t launch_tree_tc(int d, bool pair, bool quantised, int grid, int least, const CUtensorMap& tq,
+                           const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
+  if (d == 32)
+    return quantised ? launch_tc<32, false, true>(grid, least, tq, tk, tv, p, stream)
+                     : launch_tc<32, false, false>(grid, least, tq, tk, tv, p, stream);
+  if (d == 64 && !pair)
+    return quantised ? launch_tc<64, false, true>(grid, least, tq, tk, tv, p, stream)
+                     : launch_tc<64, false, false>(grid, least, tq, tk, tv, p, stream);
+  if (d == 64)
+    return quantised ? launch_tc<64, true, true>(grid, least, tq, tk, tv, p, stream)
+                     : launch_tc<64, true, false>(grid, least, tq, tk, tv, p, stream);
+  if (d == 128 && !pair)
+    return quantised ? launch_tc<128, false, true>(grid, least, tq, tk, tv, p, stream)
+                     : launch_tc<128, false, false>(grid, least, tq, tk, tv, p, stream);
+  if (d == 128)
+    return quantised ? launch_tc<128, true, true>(grid, least, tq, tk, tv, p, stream)
+                     : launch_tc<128, true, false>(grid, least, tq, tk, tv, p, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace attn

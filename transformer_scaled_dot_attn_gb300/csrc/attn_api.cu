@@ -1117,6 +1117,7 @@ int attn_decode_tree(const void* q, const void* k, const void* v, void* o, float
   p.row_blocks = plan.row_blocks;
   p.block_rows = plan.block_rows;
   p.by_unit = plan.by_unit ? 1 : 0;
+  p.lead = plan.lead;
   p.c = static_cast<float>(static_cast<double>(scale) * kLog2e);
   p.wd.status = status;
   p.wd.budget_ns = g_watchdog_ns.load();

@@ -334,6 +334,7 @@ struct TreeParams {
   int B, h_kv, n, rows, m;         // rows = (h / h_kv) n
   int row_blocks, block_rows;      // query rows of a key head in blocks of block_rows
   int by_unit;                     // a CTA for each unit (attn_tree.cuh)
+  int lead;                        // tiles' worth of time that beginning a unit takes
   float c;                         // scale log2(e)
   Watchdog wd;
 };
@@ -344,6 +345,7 @@ struct TreePlan {
   bool pair;               // ... with two CTAs on 256 rows
   int tile;                // keys of a TMA box
   int row_blocks, block_rows;
+  int lead;                // TreeParams::lead
   bool by_unit;            // a CTA for each (sequence, key head, row block); no partial results
   int grid;                // CTAs (pairs)
   long long slots;         // partial results

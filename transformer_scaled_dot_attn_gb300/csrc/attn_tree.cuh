@@ -48,8 +48,9 @@ __device__ __forceinline__ uint32_t sees32(unsigned long long word, int key, int
 __device__ __forceinline__ int tiles_of(int L, int bn) { return L > bn ? (L + bn - 1) / bn : 1; }
 
 // The work is a line of tiles: the units (sequence, key head, block of query
-// rows) one after the other, each with its sequence's tiles. CTA c of `ctas`
-// takes tiles [U c / ctas, U (c + 1) / ctas) of the U on the line: equal shares
+// rows) one after the other, each with its sequence's tiles, after `lead` places
+// that stand for the time that beginning a unit takes. CTA c of `ctas` takes the
+// places [U c / ctas, U (c + 1) / ctas) of the U on the line: equal shares
 // whatever the lengths, at the price of units that several CTAs hold a part
 // of. The part of unit x that CTA c holds has its place x + c in the partial
 // results (the sum grows from part to part along the line). A pair of CTAs that
@@ -73,7 +74,7 @@ __device__ __forceinline__ TreeLine tree_line(const TreeParams& p, int bn, int g
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   }
-  l.U = t * l.per_seq;
+  l.U = (t + static_cast<long long>(p.B) * p.lead) * l.per_seq;
   const long long most = (l.U + least - 1) / least;
   l.ctas = static_cast<int>(most < grid ? most : grid);
   return l;
@@ -85,8 +86,8 @@ __device__ __forceinline__ int tree_len(const TreeParams& p, int b) {
 
 // A CTA's position on the line: the sequence and unit it is at.
 struct TreeWalk {
-  long long pos, end;   // tiles left: [pos, end)
-  long long first;      // where the current unit begins
+  long long pos, end;   // places left: [pos, end)
+  long long first;      // where the current unit's tiles begin
   int b, idx;           // sequence, unit within the sequence
   int L, tiles;         // the sequence's cached positions and tiles
   int cta;
@@ -122,10 +123,11 @@ __device__ __forceinline__ bool tree_start(const TreeParams& p, int bn, int leas
   if (p.kv_len == nullptr) {
     w.tiles = tiles_of(p.m, bn);
     w.L = p.m;
-    const long long unit = w.pos / w.tiles;
+    const int span = w.tiles + p.lead;
+    const long long unit = w.pos / span;
     w.b = static_cast<int>(unit / l.per_seq);
     w.idx = static_cast<int>(unit - static_cast<long long>(w.b) * l.per_seq);
-    w.first = unit * w.tiles;
+    w.first = unit * span + p.lead;
     return true;
   }
   long long base = 0;
@@ -133,7 +135,7 @@ __device__ __forceinline__ bool tree_start(const TreeParams& p, int bn, int leas
     const int b = b0 + lane;
     const int L = b < p.B ? tree_len(p, b) : 0;
     const int tiles = b < p.B ? tiles_of(L, bn) : 0;
-    long long incl = static_cast<long long>(tiles) * l.per_seq;
+    long long incl = b < p.B ? static_cast<long long>(tiles + p.lead) * l.per_seq : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -145,9 +147,10 @@ __device__ __forceinline__ bool tree_start(const TreeParams& p, int bn, int leas
       w.b = b0 + src;
       w.L = __shfl_sync(0xffffffffu, L, src);
       w.tiles = __shfl_sync(0xffffffffu, tiles, src);
-      const long long at = base + __shfl_sync(0xffffffffu, incl, src) - static_cast<long long>(w.tiles) * l.per_seq;
-      w.idx = static_cast<int>((w.pos - at) / w.tiles);
-      w.first = at + static_cast<long long>(w.idx) * w.tiles;
+      const int span = w.tiles + p.lead;
+      const long long at = base + __shfl_sync(0xffffffffu, incl, src) - static_cast<long long>(span) * l.per_seq;
+      w.idx = static_cast<int>((w.pos - at) / span);
+      w.first = at + static_cast<long long>(w.idx) * span + p.lead;
       return true;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -157,6 +160,7 @@ __device__ __forceinline__ bool tree_start(const TreeParams& p, int bn, int leas
 
 // The walk's next part; false at its end.
 __device__ __forceinline__ bool tree_next(const TreeParams& p, int bn, TreeWalk& w, TreePart& s) {
+  if (w.pos < w.first) w.pos = w.first;
   if (w.pos >= w.end) return false;
   s.b = w.b;
   s.bh = w.b * p.h_kv + w.idx / p.row_blocks;
@@ -170,7 +174,7 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, int bn, TreeWalk&
   s.slot = s.unit + w.cta;
   w.pos += s.t1 - s.t0;
   if (s.t1 == w.tiles && w.pos < w.end) {
-    w.first += w.tiles;
+    w.first += w.tiles + p.lead;
     if (++w.idx == p.h_kv * p.row_blocks) {
       w.idx = 0;
       ++w.b;

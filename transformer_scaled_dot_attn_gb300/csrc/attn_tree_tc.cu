@@ -324,7 +324,8 @@ __device__ __forceinline__ int scan_bytes(const unsigned char* b, const unsigned
   if (v0 < v1) {
     const uint4* v = reinterpret_cast<const uint4*>(v0);
     const long long count = static_cast<long long>(v1 - v0) / 16;
-#pragma unroll 2
+    // (unrolled: the loads' latencies overlap)
+#pragma unroll 8
     for (long long i = t; i < count; i += 128) {
       const uint4 x = __ldg(v + i);
       m = __vmaxu4(m, __vmaxu4(__vmaxu4(x.x, x.y), __vmaxu4(x.z, x.w)));

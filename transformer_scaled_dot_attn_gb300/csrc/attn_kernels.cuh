@@ -342,7 +342,7 @@ struct TreeParams {
 // How a step is run: fixed by its sizes and cache type.
 struct TreePlan {
   bool tc;                 // the tcgen05 kernel (128-row query tiles), else mma.sync (16 rows)
-  bool pair;               // ... with two CTAs on 256 rows
+  bool pair;               // ... with two CTAs on 256 or 512 rows
   int tile;                // keys of a TMA box
   int row_blocks, block_rows;
   int lead;                // TreeParams::lead
@@ -354,7 +354,7 @@ TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised);
 cudaError_t launch_tree(int d, bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
                         const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
 // The tcgen05 kernel (attn_tree_tc.cu).
-cudaError_t launch_tree_tc(int d, bool pair, bool quantised, int grid, int least, const CUtensorMap& tq,
+cudaError_t launch_tree_tc(int d, bool quantised, int grid, int least, const CUtensorMap& tq,
                            const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
 
 }  // namespace attn

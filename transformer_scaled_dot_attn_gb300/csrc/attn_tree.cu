@@ -34,7 +34,7 @@ constexpr int kTreeRows = 16;     // query rows of a CTA (one mma.sync tile)
 constexpr int kTreeLeast = 2;     // tiles (of four warps) worth a CTA of their own
 constexpr int kTreeLeastTc = 2;   // the same for the tcgen05 kernel
 // Tiles' worth of time that beginning a unit takes. With 0, 1, 2, 3, 4: 73.0, 71.4,
-// 69.3, 69.0, 70.3 us (65 sequences of uneven lengths, 16 rows, e4m3), and 98.7 to
+// 69.3, 69.0, 70.3 us (64 sequences of uneven lengths, 16 heads of one row, e4m3), 98.7 to
 // 96.4 us from 2 on (4 sequences, 512 rows, e4m3).
 constexpr int kTreeLead = 3;
 constexpr int kTreeShort = 8;     // tiles of a cache that one CTA takes alone
@@ -742,7 +742,7 @@ template <int D>
 cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
                           const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   cudaError_t e;
-  if (plan.tc) e = launch_tree_tc(D, plan.pair, quantised, plan.grid, kTreeLeastTc, tq, tk, tv, p, stream);
+  if (plan.tc) e = launch_tree_tc(D, quantised, plan.grid, kTreeLeastTc, tq, tk, tv, p, stream);
   else if (quantised) e = launch_small_rows<D, true>(plan.grid, tk, tv, p, stream);
   else e = launch_small_rows<D, false>(plan.grid, tk, tv, p, stream);
   if (e != cudaSuccess || plan.by_unit) return e;
@@ -767,7 +767,7 @@ TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised) {
   l.tc = tree_uses_tc(rows, d, quantised);
   if (l.tc) {
     l.pair = rows > 128 && d >= 64;
-    l.block_rows = l.pair ? 256 : 128;
+    l.block_rows = !l.pair ? 128 : rows > 256 ? 512 : 256;
     l.tile = 128;
   } else {
     l.block_rows = rows < kTreeRows ? rows : kTreeRows;

@@ -47,12 +47,12 @@ using namespace sm103;
 constexpr int kBN = 128;
 constexpr float kGrow = 8.0f;  // log2 units a row maximum may run ahead of its reference
 
-template <int D, bool PAIR, bool Q8>
+template <int D, bool PAIR, int NQ, bool Q8>
 struct Tc {
   static constexpr int CTAS = PAIR ? 2 : 1;
   static constexpr int KR = kBN / CTAS;                    // keys of a K tile in this CTA
   static constexpr int DV = D / CTAS;                      // columns of a V tile in this CTA
-  static constexpr int ATOM = D >= 64 ? 64 : D;            // bf16 elements of a swizzle row (Q, K)
+  static constexpr int ATOM = D >= 64 ? 64 : D;            // 16-bit elements of a swizzle row (Q, K)
   static constexpr int NATOM = D / ATOM;
   static constexpr uint32_t SWZ = D >= 64 ? 2u : 4u;
   static constexpr uint32_t SBO = 8u * ATOM * 2u;
@@ -64,40 +64,46 @@ struct Tc {
   static constexpr uint32_t TILE = static_cast<uint32_t>(KR) * D * 2u;   // a K or V tile (the same size)
   static constexpr uint32_t QBOX = 128u * ATOM * 2u, KBOX = KR * ATOM * 2u, VBOX = kBN * ATOMV * 2u;
   static constexpr uint32_t RAW = TILE / 2;                // a tile of codes
-  static constexpr int NT = Q8 ? (D == 128 ? (PAIR ? 3 : 2) : 4) : (D == 128 ? (PAIR ? 6 : 3) : 6);  // K ring, V ring
-  static constexpr int NR = Q8 ? (D == 128 ? (PAIR ? 6 : 2) : 4) : 1;                               // code rings
+  // rings of K and of V, and of their codes: as many places as fit, six at most
+  static constexpr uint32_t ROOM = 224u * 1024u - NQ * QTILE;
+  static constexpr int least6(uint32_t n) { return n < 6 ? static_cast<int>(n) : 6; }
+  static constexpr int NT = !Q8 ? least6(ROOM / (2 * TILE)) : D < 128 ? 4 : PAIR ? 3 : 2;
+  static constexpr int NR = !Q8 ? 1 : least6((ROOM - 2 * NT * TILE) / (2 * RAW));
   static constexpr uint32_t OFF_Q = 0;
-  static constexpr uint32_t OFF_K = QTILE;
+  static constexpr uint32_t OFF_K = NQ * QTILE;
   static constexpr uint32_t OFF_V = OFF_K + NT * TILE;
   static constexpr uint32_t OFF_RK = OFF_V + NT * TILE;
   static constexpr uint32_t OFF_RV = OFF_RK + (Q8 ? NR * RAW : 0);
   static constexpr uint32_t SMEM = OFF_RV + (Q8 ? NR * RAW : 0) + 1024;  // + alignment slack
-  static_assert(SMEM <= 226u * 1024u, "shared memory");
+  static_assert(NT >= 2 && NR >= 1 && SMEM <= 225u * 1024u, "shared memory");
   static_assert(DV >= 32, "V's swizzle");
-  static constexpr int TM_O = 2 * kBN;                     // TMEM: two S buffers, then O
-  static constexpr int PRODUCER = 4, ISSUE_S = 5, ISSUE_PV = 6, CLEANER = 7, CONV_K = 8, CONV_V = 12;  // softmax: 0 - 3
-  static constexpr int THREADS = Q8 ? 512 : 256;
+  static constexpr int TM_O = 2 * kBN;                     // TMEM: two S buffers, then O of each query tile
+  static constexpr int SOFT = 4 * NQ;                      // softmax warps: 0 to SOFT - 1
+  static constexpr int PRODUCER = SOFT, ISSUE = SOFT + 1, CLEANER = SOFT + 3, CONV = SOFT + 4;  // issuers: ISSUE, + 1
+  static constexpr int CONVERTERS = !Q8 ? 0 : NQ == 2 ? 4 : 8;  // one group of four warps for K and V, or one each
+  static constexpr int THREADS = (CONV + CONVERTERS) * 32;
   static constexpr uint32_t FORMAT = Q8 ? (1u << 7) | (1u << 10) : 0u;  // cleared from bf16's descriptor: f16 operands
   // registers: the split must fit in what the CTA is launched with
-  static constexpr bool SPLIT = Q8;
-  static constexpr int R_SOFT = 208, R_CTRL = 64, R_CONV = 112;
-  static constexpr int R_SUM = 128 * R_SOFT + 128 * R_CTRL + 256 * R_CONV;
-  static_assert(!SPLIT || R_SUM <= 128 * THREADS, "register split");
+  static constexpr bool SPLIT = Q8 || NQ == 2;
+  static constexpr int R_SOFT = Q8 && NQ == 2 ? 176 : 208, R_CTRL = !Q8 ? 88 : NQ == 2 ? 72 : 64;
+  static constexpr int R_CONV = NQ == 2 ? 88 : 112;
+  static constexpr int R_SUM = 32 * (SOFT * R_SOFT + 4 * R_CTRL + CONVERTERS * R_CONV);
+  static_assert(!SPLIT || R_SUM <= 65536 / THREADS / 8 * 8 * THREADS, "register split");
 };
 
 constexpr int kMaxRing = 6;
 
 struct TcShared {
   uint64_t q_full, q_empty;                    // TMA; released by the part's last scores
-  uint64_t q_ready;                            // Q is there (e4m3: in f16) [issuer]
+  uint64_t q_ready[2];                         // a query tile is there (e4m3: in f16) [issuer]
   uint64_t k_tma[kMaxRing], v_tma[kMaxRing];   // bf16: tile loaded
   uint64_t k_ready[kMaxRing], v_ready[kMaxRing];  // tile can be multiplied [issuer]
-  uint64_t k_empty[kMaxRing], v_empty[kMaxRing];  // S, P V of the tile complete
+  uint64_t k_empty[kMaxRing], v_empty[kMaxRing];  // S, P V of the tile complete, of every query tile
   uint64_t raw_full[2][kMaxRing], raw_empty[2][kMaxRing];  // e4m3: codes of K, V
   uint64_t scanned[2];                         // e4m3: the part's scales of K, V were looked at
   uint64_t s_full[2];                          // by S buffer
   uint64_t p_full[2][2];                       // S buffer, half of the tile's keys [issuer]
-  uint64_t o_free;                             // [issuer]
+  uint64_t o_full[2], o_free[2];               // by query tile: the part's O is complete; has been read
   uint64_t drain[2];                           // by issuer
   uint32_t tmem_base;
   int abort_flag;
@@ -316,28 +322,27 @@ __device__ __forceinline__ uint32_t pack_f16x2_pair(uint64_t v) {
   return pack_f16x2(lo, hi);
 }
 
-// The largest of the bytes [b, e), this thread's share of 128.
-__device__ __forceinline__ int scan_bytes(const unsigned char* b, const unsigned char* e, int t) {
-  const uintptr_t v0 = (reinterpret_cast<uintptr_t>(b) + 15) & ~static_cast<uintptr_t>(15);
-  const uintptr_t v1 = reinterpret_cast<uintptr_t>(e) & ~static_cast<uintptr_t>(15);
+// The largest of the bytes [b, e), this thread's share of 128. (Four loads at a
+// time, whose latencies overlap.)
+__device__ __forceinline__ uint32_t scan_bytes(const unsigned char* b, const unsigned char* e, int t) {
+  const uintptr_t v0 = min((reinterpret_cast<uintptr_t>(b) + 15) & ~static_cast<uintptr_t>(15),
+                           reinterpret_cast<uintptr_t>(e));
+  const uintptr_t v1 = max(reinterpret_cast<uintptr_t>(e) & ~static_cast<uintptr_t>(15), v0);
+  const uint4* v = reinterpret_cast<const uint4*>(v0);
+  const long long count = static_cast<long long>(v1 - v0) / 16;
   uint32_t m = 0;
-  if (v0 < v1) {
-    const uint4* v = reinterpret_cast<const uint4*>(v0);
-    const long long count = static_cast<long long>(v1 - v0) / 16;
-    // (unrolled: the loads' latencies overlap)
-#pragma unroll 8
-    for (long long i = t; i < count; i += 128) {
-      const uint4 x = __ldg(v + i);
-      m = __vmaxu4(m, __vmaxu4(__vmaxu4(x.x, x.y), __vmaxu4(x.z, x.w)));
-    }
-    const unsigned char* head = reinterpret_cast<const unsigned char*>(v0);
-    const unsigned char* tail = reinterpret_cast<const unsigned char*>(v1);
-    if (b + t < head) m = __vmaxu4(m, static_cast<uint32_t>(__ldg(b + t)));
-    if (tail + t < e) m = __vmaxu4(m, static_cast<uint32_t>(__ldg(tail + t)));
-  } else {
-    for (const unsigned char* x = b + t; x < e; x += 128) m = __vmaxu4(m, static_cast<uint32_t>(__ldg(x)));
+  if (b + t < reinterpret_cast<const unsigned char*>(v0)) m = __ldg(b + t);
+  if (reinterpret_cast<const unsigned char*>(v1) + t < e)
+    m = max(m, static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned char*>(v1) + t)));
+#pragma unroll 1
+  for (long long i = t; i < count; i += 512) {
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = i + u * 128 < count ? __ldg(v + i + u * 128) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m = __vmaxu4(m, __vmaxu4(__vmaxu4(x[u].x, x[u].y), __vmaxu4(x[u].z, x[u].w)));
   }
-  return static_cast<int>(max(max(m & 0xffu, (m >> 8) & 0xffu), max((m >> 16) & 0xffu, m >> 24)));
+  return max(max(m & 0xffu, (m >> 8) & 0xffu), max((m >> 16) & 0xffu, m >> 24));
 }
 
 // The value at column c of a position, for the rare rows that add one that is not finite themselves.
@@ -364,11 +369,11 @@ __device__ __forceinline__ void mark_odd(TcShared& sh, int seg, uint32_t rank) {
                  : "memory");
 }
 
-template <int D, bool PAIR, bool Q8>
-__global__ void __launch_bounds__(Tc<D, PAIR, Q8>::THREADS, 1)
+template <int D, bool PAIR, int NQ, bool Q8>
+__global__ void __launch_bounds__(Tc<D, PAIR, NQ, Q8>::THREADS, 1)
 attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const TreeParams p, int least) {
-  using C = Tc<D, PAIR, Q8>;
+  using C = Tc<D, PAIR, NQ, Q8>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) TcShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -381,39 +386,45 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   TreeWalk walk;
   if (!tree_start(p, kBN, least, static_cast<int>(blockIdx.x) / C::CTAS, static_cast<int>(gridDim.x) / C::CTAS, walk))
     return;  // (both CTAs of a pair, or neither)
-  if (tid == 0) {
-    mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
-    mbar_init(&sh.q_ready, Q8 ? 4 * C::CTAS : C::CTAS);
-    for (int s = 0; s < C::NT; ++s) {
-      mbar_init(&sh.k_tma[s], 1);
-      mbar_init(&sh.v_tma[s], 1);
-      mbar_init(&sh.k_ready[s], Q8 ? 4 * C::CTAS : C::CTAS);
-      mbar_init(&sh.v_ready[s], Q8 ? 4 * C::CTAS : C::CTAS);
-      mbar_init(&sh.k_empty[s], 1);
-      mbar_init(&sh.v_empty[s], 1);
+  if (warp == C::PRODUCER) {
+    // (a lane a place of the rings)
+    if (lane < C::NT) {
+      mbar_init(&sh.k_tma[lane], 1);
+      mbar_init(&sh.v_tma[lane], 1);
+      mbar_init(&sh.k_ready[lane], Q8 ? 4 * C::CTAS : C::CTAS);
+      mbar_init(&sh.v_ready[lane], Q8 ? 4 * C::CTAS : C::CTAS);
+      mbar_init(&sh.k_empty[lane], 1);
+      mbar_init(&sh.v_empty[lane], 1);
     }
-    for (int u = 0; u < 2; ++u) {
-      for (int s = 0; s < C::NR; ++s) {
-        mbar_init(&sh.raw_full[u][s], 1);
-        mbar_init(&sh.raw_empty[u][s], 4);
+    if (lane < C::NR)
+      for (int kind = 0; kind < 2; ++kind) {
+        mbar_init(&sh.raw_full[kind][lane], 1);
+        mbar_init(&sh.raw_empty[kind][lane], 4);
       }
-      mbar_init(&sh.scanned[u], 4);
-      mbar_init(&sh.s_full[u], 1);
-      mbar_init(&sh.p_full[u][0], 4 * C::CTAS);
-      mbar_init(&sh.p_full[u][1], 4 * C::CTAS);
+    if (lane < 2) {
+      mbar_init(&sh.q_ready[lane], Q8 ? 4 * C::CTAS : C::CTAS);
+      mbar_init(&sh.scanned[lane], 4);
+      mbar_init(&sh.s_full[lane], 1);
+      mbar_init(&sh.p_full[lane][0], 4 * C::CTAS);
+      mbar_init(&sh.p_full[lane][1], 4 * C::CTAS);
+      mbar_init(&sh.o_full[lane], 1);
+      mbar_init(&sh.o_free[lane], 4 * C::CTAS);
+      mbar_init(&sh.drain[lane], 1);
     }
-    mbar_init(&sh.o_free, 4 * C::CTAS);
-    mbar_init(&sh.drain[0], 1);
-    mbar_init(&sh.drain[1], 1);
-    sh.abort_flag = 0;
-    for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
+    if (lane < 4) sh.odd[lane] = 0;
+    if (lane == 0) {
+      mbar_init(&sh.q_full, 1);
+      mbar_init(&sh.q_empty, 1);
+      sh.abort_flag = 0;
+      prefetch_tensormap(&tm_q);
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+    }
     fence_mbar_init();
-    prefetch_tensormap(&tm_q);
-    prefetch_tensormap(&tm_k);
-    prefetch_tensormap(&tm_v);
   }
-  if (warp == C::ISSUE_S) tc_alloc<PAIR>(&sh.tmem_base);
+  if (warp == C::ISSUE) {
+    tc_alloc<PAIR>(&sh.tmem_base);
+  }
   tc_fence_before();
   __syncthreads();
   if (PAIR) cluster_sync();  // the other CTA's barriers are there
@@ -427,19 +438,19 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     return tc_wait<PAIR>(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, wd, site);
   };
 
-  if (warp < 4) {
+  if (warp < C::SOFT) {
     // ------------------------------------------------------------ softmax, one thread a row
     if (C::SPLIT) reg_alloc<C::R_SOFT>();
-    const int r = tid;
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t t_o = tmem + lane_base + C::TM_O;
+    const int tile = warp >> 2, r = tid & 127;  // query tile, its row
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_o = tmem + lane_base + C::TM_O + tile * D;
     // e4m3: weights against a reference this far below the maximum (log2 units)
     constexpr float kLow = Q8 ? 7.f : 0.f;
 #pragma unroll 1
     while (ok && tree_next(p, kBN, walk, part)) {
       const int old = part.L - p.n;
-      const int at = static_cast<int>(rank) * 128 + r;  // row of the block
-      const int row = part.rb * (128 * C::CTAS) + at;
+      const int at = (tile * C::CTAS + static_cast<int>(rank)) * 128 + r;  // row of the block
+      const int row = part.rb * (128 * C::CTAS * NQ) + at;
       const bool real = row < p.rows;
       const bool idle = __all_sync(0xffffffffu, !real);  // this warp's rows do not exist
       const unsigned long long word = real ? tree_word(p, part.b, row) : 0ull;
@@ -449,12 +460,12 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if constexpr (Q8) {
         ok = __all_sync(0xffffffffu, wait(&sh.q_full, seg, kSiteQFull));
         if (!ok) break;
-        uint8_t* tile = smem + C::OFF_Q;
+        uint8_t* sq = smem + C::OFF_Q + tile * C::QTILE;
         uint4 w[D / 8];
         uint32_t top = 0;
 #pragma unroll
         for (int cc = 0; cc < D / 8; ++cc) {
-          w[cc] = *reinterpret_cast<const uint4*>(tile + chunk_off<D, 128>(r, cc));
+          w[cc] = *reinterpret_cast<const uint4*>(sq + chunk_off<D, 128>(r, cc));
           top = max(top, max(max(finite_top(w[cc].x), finite_top(w[cc].y)), max(finite_top(w[cc].z), finite_top(w[cc].w))));
         }
         const uint32_t up = 268u - max(top >> 7, 15u);
@@ -462,18 +473,18 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         c *= __uint_as_float((254u - up) << 23);
 #pragma unroll
         for (int cc = 0; cc < D / 8; ++cc)
-          *reinterpret_cast<uint4*>(tile + chunk_off<D, 128>(r, cc)) =
+          *reinterpret_cast<uint4*>(sq + chunk_off<D, 128>(r, cc)) =
               make_uint4(to_f16(w[cc].x, f), to_f16(w[cc].y, f), to_f16(w[cc].z, f), to_f16(w[cc].w, f));
         fence_proxy_async_smem();
-        tell_issuer<PAIR>(&sh.q_ready);
+        tell_issuer<PAIR>(&sh.q_ready[tile]);
       }
       float m_used = -INFINITY, l = 0.f;
       uint64_t c2 = f2_pack(c, c);
 #pragma unroll 1
       for (int j = 0; j < T; ++j) {
-        const int gi = done + j, u = gi & 1;
+        const int gi = done + j, u = NQ == 2 ? tile : gi & 1;
         const uint32_t t_s = tmem + lane_base + u * kBN;
-        ok = __all_sync(0xffffffffu, wait(&sh.s_full[u], gi >> 1, kSiteSFull));
+        ok = __all_sync(0xffffffffu, wait(&sh.s_full[u], NQ == 2 ? gi : gi >> 1, kSiteSFull));
         if (!ok) break;
         tc_fence_after();
         if (Q8 && j == 0) {  // the part's largest K scale is known by now
@@ -483,7 +494,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (idle) {
           tc_fence_before();
           tell_issuer<PAIR>(&sh.p_full[u][0]);
-          tell_issuer<PAIR>(&sh.p_full[u][1]);
+          if (NQ == 1) tell_issuer<PAIR>(&sh.p_full[u][1]);
           continue;
         }
         uint32_t s[4][32];
@@ -523,10 +534,13 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const float m_ref = m_used == -INFINITY ? 0.f : m_used - kLow;  // nothing seen yet: weights 0
         const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
         if (j > 0 && __any_sync(0xffffffffu, moved)) {
-          // the products so far are in O (the scores, a buffer ahead, do not show that)
-          ok = __all_sync(0xffffffffu, wait(&sh.v_empty[(gi - 1) % C::NT], (gi - 1) / C::NT, kSitePFull));
-          if (!ok) break;
-          tc_fence_after();
+          // the products so far are in O (two query tiles: the scores came after
+          // them; the scores of one, a buffer ahead, do not show that)
+          if (NQ == 1) {
+            ok = __all_sync(0xffffffffu, wait(&sh.v_empty[(gi - 1) % C::NT], (gi - 1) / C::NT, kSitePFull));
+            if (!ok) break;
+            tc_fence_after();
+          }
           tc_rescale<D>(t_o, alpha);
           l *= alpha;
         }
@@ -550,9 +564,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             tmem_st16(t_s + q * 16, pk);
           }
+          if (NQ == 2 && half == 0) continue;  // (the issuer is with the other query tile)
           tmem_st_wait();
           tc_fence_before();
-          tell_issuer<PAIR>(&sh.p_full[u][half]);
+          tell_issuer<PAIR>(&sh.p_full[u][NQ == 1 ? half : 0]);
         }
         float a0, a1, a2, a3;
         f2_unpack(acc0, a0, a1);
@@ -561,7 +576,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       }
       // the last tile's product
       done += T;
-      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.v_empty[(done - 1) % C::NT], (done - 1) / C::NT, kSiteOFull));
+      if (ok) ok = __all_sync(0xffffffffu, wait(&sh.o_full[tile], seg, kSiteOFull));
       if (!ok) break;
       tc_fence_after();
       if (!idle) {
@@ -617,100 +632,111 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
       }
       tc_fence_before();
-      tell_issuer<PAIR>(&sh.o_free);
+      tell_issuer<PAIR>(&sh.o_free[tile]);
       ++seg;
     }
-  } else if (Q8 && warp >= C::CONV_K) {
-    // ------------------------------------------------------------ converters
+  } else if (Q8 && warp >= C::CONV) {
+    // ------------------------------------------------------------ converters, one thread a row of K, V or both
     if (C::SPLIT) reg_dealloc<C::R_CONV>();
-    const bool is_v = warp >= C::CONV_V;
-    const int t = tid - (is_v ? C::CONV_V : C::CONV_K) * 32, wi = t >> 5;
-    // a thread converts one row of V, or of K (pair: one of the halves of a row)
-    const int r = is_v ? t : t % C::KR;
-    const int c0 = is_v ? 0 : t / C::KR * (C::DV / 16);  // first 16-byte chunk
-    const unsigned char* exps = is_v ? p.v_exp : p.k_exp;
-    uint8_t* ring = smem + (is_v ? C::OFF_V : C::OFF_K);
-    const uint8_t* raw = smem + (is_v ? C::OFF_RV : C::OFF_RK);
-    uint64_t* ready = is_v ? sh.v_ready : sh.k_ready;
-    uint64_t* empty = is_v ? sh.v_empty : sh.k_empty;
+    const int t = tid & 127;
+    const int first_kind = NQ == 2 ? 0 : (warp - C::CONV) >> 2, last_kind = NQ == 2 ? 1 : first_kind;  // 0: K, 1: V
+    uint64_t* scanned = &sh.scanned[first_kind];
+    // This thread's row of a tile and, as K tiles of a pair have 64 rows, its half
+    // of the row; of the sequence's tile, whose other half the pair's other CTA has.
+    const int row_of[2] = {t % C::KR, t}, c0[2] = {t / C::KR * (C::DV / 16), 0};
+    const int first_row[2] = {static_cast<int>(rank) * C::KR + row_of[0], t};
 #pragma unroll 1
     while (ok && tree_next(p, kBN, walk, part)) {
       const int old = part.L - p.n, T = part.t1 - part.t0;
-      const unsigned char* row = exps + static_cast<size_t>(part.bh) * p.m;
-      const int key_end = min(part.L, part.t1 * kBN);
-      // the largest scale of the part's keys
-      int top = scan_bytes(row + min(part.t0 * kBN, key_end), row + key_end, t);
-      top = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top)));
-      if (lane == 0) sh.scan[seg & 3][is_v][wi] = top;
+      const size_t base = static_cast<size_t>(part.bh) * p.m;
+      const int key_begin = part.t0 * kBN, key_end = min(part.L, part.t1 * kBN);
+      int top[2] = {0, 0}, byte[2] = {0, 0};
+      uint32_t most[2] = {0, 0};
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        if (kind < first_kind || kind > last_kind) continue;
+        // the largest scale of the part's keys
+        const unsigned char* row = (kind == 0 ? p.k_exp : p.v_exp) + base;
+        const int key = key_begin + first_row[kind];
+        if (key < key_end) byte[kind] = __ldg(row + key);  // read a tile ahead
+        most[kind] = scan_bytes(row + min(key_begin, key_end), row + key_end, t);
+      }
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        if (kind < first_kind || kind > last_kind) continue;
+        const unsigned all = __reduce_max_sync(0xffffffffu, most[kind]);
+        if (lane == 0) sh.scan[seg & 3][kind][warp & 3] = static_cast<int>(all);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.scanned[is_v]);
-      ok = __all_sync(0xffffffffu, guarded_wait(&sh.scanned[is_v], seg & 1, abort_flag, wd, kSiteKFull));
+      if (lane == 0) mbar_arrive(scanned);
+      ok = __all_sync(0xffffffffu, guarded_wait(scanned, seg & 1, abort_flag, wd, kSiteKFull));
       if (!ok) break;
-      const int* of = sh.scan[seg & 3][is_v];
-      top = max(max(of[0], of[1]), max(of[2], of[3]));
-      if (t == 0) sh.ref[seg & 3][is_v] = top;
-      const int first = part.t0 * kBN + (is_v ? 0 : static_cast<int>(rank) * C::KR) + r;  // this thread's key of a tile
-      int byte = first < key_end ? __ldg(row + first) : 0;  // read a tile ahead
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        const int* of = sh.scan[seg & 3][kind];
+        if (kind < first_kind || kind > last_kind) continue;
+        top[kind] = max(max(of[0], of[1]), max(of[2], of[3]));
+        if (t == 0) sh.ref[seg & 3][kind] = top[kind];
+      }
 #pragma unroll 1
-      for (int j = 0; j < T; ++j) {
-        const uint32_t f = pow2_f16x2(byte - top + 7);
-        const int key = first + j * kBN;
-        if (key + kBN < key_end) byte = __ldg(row + key + kBN);
-        const int gi = done + j, rs = gi % C::NR, bs = gi % C::NT;
-        ok = guarded_wait(&sh.raw_full[is_v][rs], (gi / C::NR) & 1, abort_flag, wd, kSiteKFull) &&
-             (gi < C::NT || wait(&empty[bs], gi / C::NT - 1, kSiteKEmpty));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint8_t* src = raw + rs * C::RAW;
-        uint8_t* dst = ring + bs * C::TILE;
-        if (!is_v) {
+      for (int x = 0; ok && x < T + last_kind; ++x) {
 #pragma unroll
-          for (int cc = 0; cc < C::DV / 16; ++cc) {
-            const uint4 w = *reinterpret_cast<const uint4*>(src + raw_off<D>(r, c0 + cc));
-            *reinterpret_cast<uint4*>(dst + chunk_off<D, C::KR>(r, 2 * (c0 + cc))) =
-                make_uint4(codes_f16(w.x & 0xffffu, f), codes_f16(w.x >> 16, f), codes_f16(w.y & 0xffffu, f),
-                           codes_f16(w.y >> 16, f));
-            *reinterpret_cast<uint4*>(dst + chunk_off<D, C::KR>(r, 2 * (c0 + cc) + 1)) =
-                make_uint4(codes_f16(w.z & 0xffffu, f), codes_f16(w.z >> 16, f), codes_f16(w.w & 0xffffu, f),
-                           codes_f16(w.w >> 16, f));
-          }
-        } else if ((part.t0 + j + 1) * kBN <= old) {
+        for (int kind = 0; kind < 2; ++kind) {
+          const int j = x - kind, gi = done + j, key = key_begin + j * kBN + first_row[kind];  // (V a tile behind)
+          if (kind < first_kind || kind > last_kind || j < 0 || j >= T) continue;
+          const int rs = gi % C::NR, bs = gi % C::NT, r = row_of[kind];
+          const uint32_t f = pow2_f16x2(byte[kind] - top[kind] + 7);
+          if (key + kBN < key_end) byte[kind] = __ldg((kind == 0 ? p.k_exp : p.v_exp) + base + key + kBN);
+          ok = guarded_wait(&sh.raw_full[kind][rs], (gi / C::NR) & 1, abort_flag, wd, kSiteKFull) &&
+               (gi < C::NT || wait(kind == 0 ? &sh.k_empty[bs] : &sh.v_empty[bs], gi / C::NT - 1, kSiteKEmpty));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* src = smem + (kind == 0 ? C::OFF_RK : C::OFF_RV) + rs * C::RAW;
+          uint8_t* dst = smem + (kind == 0 ? C::OFF_K : C::OFF_V) + bs * C::TILE;
+          // (an f16 tile's chunks: K has rows of D, V of DV)
+          auto from = [&](int cc) {
+            return *reinterpret_cast<const uint4*>(src + (kind == 0 ? raw_off<D>(r, c0[0] + cc) : raw_off<C::DV>(r, cc)));
+          };
+          auto to = [&](int cc) {
+            return reinterpret_cast<uint4*>(
+                dst + (kind == 0 ? chunk_off<D, C::KR>(r, 2 * c0[0] + cc) : chunk_off<C::DV, kBN>(r, cc)));
+          };
+          if (kind == 0 || (part.t0 + j + 1) * kBN <= old) {
 #pragma unroll
-          for (int cc = 0; cc < C::DV / 16; ++cc) {
-            const uint4 w = *reinterpret_cast<const uint4*>(src + raw_off<C::DV>(r, cc));
-            *reinterpret_cast<uint4*>(dst + chunk_off<C::DV, kBN>(r, 2 * cc)) =
-                make_uint4(codes_f16(w.x & 0xffffu, f), codes_f16(w.x >> 16, f), codes_f16(w.y & 0xffffu, f),
-                           codes_f16(w.y >> 16, f));
-            *reinterpret_cast<uint4*>(dst + chunk_off<C::DV, kBN>(r, 2 * cc + 1)) =
-                make_uint4(codes_f16(w.z & 0xffffu, f), codes_f16(w.z >> 16, f), codes_f16(w.w & 0xffffu, f),
-                           codes_f16(w.w >> 16, f));
-          }
-        } else {
-          // Rows past the sequence are anyone's: zeros. NaN codes become zeros
-          // too (a weight of 0 would make them NaN for rows that do not see
-          // them); the rows that do see them add them at the end.
-          const bool zero = key >= part.L;
-          bool odd = false;
-          for (int cc = 0; cc < C::DV / 16; ++cc) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(src + raw_off<C::DV>(r, cc));
-            uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t n = nan_codes(w[i]) & 0x80808080u;
-              odd |= n != 0;
-              w[i] = zero ? 0u : w[i] & ~((n >> 7) * 0xffu);
-              o[2 * i] = codes_f16(w[i] & 0xffffu, f);
-              o[2 * i + 1] = codes_f16(w[i] >> 16, f);
+            for (int cc = 0; cc < C::DV / 16; ++cc) {
+              const uint4 w = from(cc);
+              *to(2 * cc) = make_uint4(codes_f16(w.x & 0xffffu, f), codes_f16(w.x >> 16, f),
+                                       codes_f16(w.y & 0xffffu, f), codes_f16(w.y >> 16, f));
+              *to(2 * cc + 1) = make_uint4(codes_f16(w.z & 0xffffu, f), codes_f16(w.z >> 16, f),
+                                           codes_f16(w.w & 0xffffu, f), codes_f16(w.w >> 16, f));
             }
-            *reinterpret_cast<uint4*>(dst + chunk_off<C::DV, kBN>(r, 2 * cc)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + chunk_off<C::DV, kBN>(r, 2 * cc + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+          } else {
+            // Rows past the sequence are anyone's: zeros. NaN codes become zeros
+            // too (a weight of 0 would make them NaN for rows that do not see
+            // them); the rows that do see them add them at the end.
+            const bool zero = key >= part.L;
+            bool odd = false;
+            for (int cc = 0; cc < C::DV / 16; ++cc) {
+              const uint4 w4 = from(cc);
+              uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t n = nan_codes(w[i]) & 0x80808080u;
+                odd |= n != 0;
+                w[i] = zero ? 0u : w[i] & ~((n >> 7) * 0xffu);
+                o[2 * i] = codes_f16(w[i] & 0xffffu, f);
+                o[2 * i + 1] = codes_f16(w[i] >> 16, f);
+              }
+              *to(2 * cc) = make_uint4(o[0], o[1], o[2], o[3]);
+              *to(2 * cc + 1) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            if (odd && !zero) mark_odd<PAIR>(sh, seg, rank);
           }
-          if (odd && !zero) mark_odd<PAIR>(sh, seg, rank);
+          fence_proxy_async_smem();
+          tell_issuer<PAIR>(kind == 0 ? &sh.k_ready[bs] : &sh.v_ready[bs]);
+          if (lane == 0) mbar_arrive(&sh.raw_empty[kind][rs]);
         }
-        fence_proxy_async_smem();
-        tell_issuer<PAIR>(&ready[bs]);
-        if (lane == 0) mbar_arrive(&sh.raw_empty[is_v][rs]);
       }
       done += T;
       ++seg;
@@ -722,132 +748,179 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (lane == 0) {
         constexpr int N = Q8 ? C::NR : C::NT;
         constexpr uint32_t BYTES = Q8 ? C::RAW : C::TILE;
-        uint64_t* kf = Q8 ? sh.raw_full[0] : sh.k_tma;
-        uint64_t* vf = Q8 ? sh.raw_full[1] : sh.v_tma;
-        uint64_t* ke = Q8 ? sh.raw_empty[0] : sh.k_empty;
-        uint64_t* ve = Q8 ? sh.raw_empty[1] : sh.v_empty;
-        uint8_t* kd = smem + (Q8 ? C::OFF_RK : C::OFF_K);
-        uint8_t* vd = smem + (Q8 ? C::OFF_RV : C::OFF_V);
-        int k_loaded = 0, v_loaded = 0, q_loaded = 0;
+        const uint32_t off[2] = {Q8 ? C::OFF_RK : C::OFF_K, Q8 ? C::OFF_RV : C::OFF_V};
+        uint64_t* full[2] = {Q8 ? sh.raw_full[0] : sh.k_tma, Q8 ? sh.raw_full[1] : sh.v_tma};
+        uint64_t* empty[2] = {Q8 ? sh.raw_empty[0] : sh.k_empty, Q8 ? sh.raw_empty[1] : sh.v_empty};
+        int loaded[2] = {0, 0}, q_loaded = 0;
 #pragma unroll 1
         while (ok && tree_next(p, kBN, walk, part)) {
           const int T = part.t1 - part.t0;
           if (seg > 0) ok = wait(&sh.q_empty, seg - 1, kSiteQFull);
           if (!ok) break;
-          const int q0 = part.rb * (128 * C::CTAS) + static_cast<int>(rank) * 128;
-          mbar_arrive_expect_tx(&sh.q_full, C::QTILE);
+          mbar_arrive_expect_tx(&sh.q_full, NQ * C::QTILE);
           ++q_loaded;
-          for (int a = 0; a < C::NATOM; ++a)  // (rows past the last load as zeros)
-            tma_load_3d(smem + C::OFF_Q + a * C::QBOX, &tm_q, &sh.q_full, a * C::ATOM, q0, part.bh);
+          for (int x = 0; x < NQ * C::NATOM; ++x)  // (rows past the last load as zeros)
+            tma_load_3d(smem + C::OFF_Q + x * C::QBOX, &tm_q, &sh.q_full, x % C::NATOM * C::ATOM,
+                        ((part.rb * NQ + x / C::NATOM) * C::CTAS + static_cast<int>(rank)) * 128, part.bh);
+#pragma unroll 1
           for (int j = 0; ok && j < T; ++j) {
-            const int gi = done + j, st = gi % N;
-            const int k0 = (part.t0 + j) * kBN;
-            const int kk = k0 + static_cast<int>(rank) * C::KR, vc = static_cast<int>(rank) * C::DV;
-            if (gi >= N) ok = wait(&ke[st], gi / N - 1, kSiteKEmpty);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&kf[st], BYTES);
-            if (Q8) {
-              tma_load_3d(kd + st * BYTES, &tm_k, &kf[st], 0, kk, part.bh);
-            } else {
-              for (int a = 0; a < C::NATOM; ++a)
-                tma_load_3d(kd + st * BYTES + a * C::KBOX, &tm_k, &kf[st], a * C::ATOM, kk, part.bh);
+            const int gi = done + j, k0 = (part.t0 + j) * kBN;
+#pragma unroll
+            for (int kind = 0; kind < 2; ++kind) {
+              const int st = gi % N;
+              uint64_t* bar = &full[kind][st];
+              uint8_t* dst = smem + off[kind] + st * BYTES;
+              if (gi >= N) ok = wait(&empty[kind][st], gi / N - 1, kind == 0 ? kSiteKEmpty : kSiteVEmpty);
+              if (!ok) break;
+              mbar_arrive_expect_tx(bar, BYTES);
+              const int kk = k0 + static_cast<int>(rank) * C::KR, vc = static_cast<int>(rank) * C::DV;
+              if (kind == 0) {
+                for (int a = 0; a < (Q8 ? 1 : C::NATOM); ++a)
+                  tma_load_3d(dst + a * C::KBOX, &tm_k, bar, a * C::ATOM, kk, part.bh);
+              } else {
+                for (int a = 0; a < (Q8 ? 1 : C::NATOMV); ++a)
+                  tma_load_3d(dst + a * C::VBOX, &tm_v, bar, vc + a * C::ATOMV, k0, part.bh);
+              }
+              ++loaded[kind];
             }
-            ++k_loaded;
-            if (gi >= N) ok = wait(&ve[st], gi / N - 1, kSiteVEmpty);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&vf[st], BYTES);
-            if (Q8) {
-              tma_load_3d(vd + st * BYTES, &tm_v, &vf[st], vc, k0, part.bh);
-            } else {
-              for (int a = 0; a < C::NATOMV; ++a)
-                tma_load_3d(vd + st * BYTES + a * C::VBOX, &tm_v, &vf[st], vc + a * C::ATOMV, k0, part.bh);
-            }
-            ++v_loaded;
           }
           done += T;
           ++seg;
         }
         // every copy lands before shared memory is released
         if (q_loaded > 0) tc_drain(&sh.q_full, (q_loaded - 1) & 1, wd);
-        for (int x = max(0, k_loaded - N); x < k_loaded; ++x) tc_drain(&kf[x % N], (x / N) & 1, wd);
-        for (int x = max(0, v_loaded - N); x < v_loaded; ++x) tc_drain(&vf[x % N], (x / N) & 1, wd);
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind)
+          for (int x = max(0, loaded[kind] - N); x < loaded[kind]; ++x)
+            tc_drain(&full[kind][x % N], (x / N) & 1, wd);
       }
-    } else if (warp == C::ISSUE_S) {
-      // ---------------------------------------------------------- S (the pair's first CTA)
-      if (rank == 0 && lane == 0) {
-        const uint32_t idesc =
-            (idesc_bf16_f32(128 * C::CTAS, kBN, false, false) & ~C::FORMAT) | (p.c < 0.f ? (1u << 13) : 0u);
-        const Desc dq(smem_u32(smem + C::OFF_Q), 16, C::SBO, C::SWZ), dk(smem_u32(smem + C::OFF_K), 16, C::SBO, C::SWZ);
-        uint64_t* kr = (Q8 || PAIR) ? sh.k_ready : sh.k_tma;
-        uint64_t* qr = (Q8 || PAIR) ? &sh.q_ready : &sh.q_full;
+    } else if (warp == C::ISSUE || (NQ == 1 && warp == C::ISSUE + 1)) {
+      // ---------------------------------------------------------- issuers (the pair's first CTA)
+      // (The whole warp walks along, so that descriptors stay in uniform registers.)
+      const int who = warp - C::ISSUE;
+      const uint32_t idesc_s =
+          (idesc_bf16_f32(128 * C::CTAS, kBN, false, false) & ~C::FORMAT) | (p.c < 0.f ? (1u << 13) : 0u);
+      const uint32_t idesc_o = idesc_bf16_f32(128 * C::CTAS, D, false, true) & ~C::FORMAT;
+      const Desc dq(smem_u32(smem + C::OFF_Q), 16, C::SBO, C::SWZ), dk(smem_u32(smem + C::OFF_K), 16, C::SBO, C::SWZ);
+      const Desc dv(smem_u32(smem + C::OFF_V), C::VBOX, C::SBOV, C::SWZV);
+      auto all_wait = [&](uint64_t* bar, int phase, uint32_t site) {
+        return __all_sync(0xffffffffu, wait(bar, phase, site)) != 0;
+      };
+      // (several barriers at once: each lane looks at one of them)
+      auto wait_both = [&](uint64_t* a, int phase_a, uint64_t* b, int phase_b, uint32_t site) {
+        return all_wait(lane & 1 ? b : a, lane & 1 ? phase_b : phase_a, site);
+      };
+      auto q_there = [&](int tile) { return Q8 ? &sh.q_ready[tile] : PAIR ? &sh.q_ready[0] : &sh.q_full; };
+      auto k_there = [&](int gi) { return Q8 || PAIR ? &sh.k_ready[gi % C::NT] : &sh.k_tma[gi % C::NT]; };
+      auto v_there = [&](int gi) { return &sh.v_ready[gi % C::NT]; };
+      // S of key tile gi and query tile `tile` into buffer u
+      auto scores = [&](int gi, int tile, int u) {
+        const int st = gi % C::NT;
+        const uint32_t at = st * C::TILE, aq = tile * C::QTILE;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int a = k / (C::ATOM / 16), w = k % (C::ATOM / 16);
+            tc_mma_ss<PAIR>(tmem + u * kBN, dq.at(aq + a * C::QBOX + w * 32), dk.at(at + a * C::KBOX + w * 32), idesc_s,
+                            k > 0 ? 1u : 0u);
+          }
+          tc_commit<PAIR>(&sh.s_full[u]);
+          if (tile == NQ - 1) tc_commit<PAIR>(&sh.k_empty[st]);
+        }
+        __syncwarp();
+      };
+      // O (+)= P V of 16-key steps [k0, k1) of the same, P in buffer u
+      auto products = [&](int gi, int tile, int u, int k0, int k1, bool first) {
+        const int st = gi % C::NT;
+        const uint32_t at = st * C::TILE, t_o = tmem + C::TM_O + tile * D;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = k0; k < k1; ++k)
+            tc_mma_ts<PAIR>(t_o, tmem + u * kBN + k * 8, dv.at(at + k * 16 * C::ATOMV * 2), idesc_o,
+                            (!first || k > 0) ? 1u : 0u);
+          if (k1 == kBN / 16 && tile == NQ - 1) tc_commit<PAIR>(&sh.v_empty[st]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit<PAIR>(bar);
+        __syncwarp();
+      };
+      if (rank == 0) {
 #pragma unroll 1
-        while (ok && tree_next(p, kBN, walk, part)) {
-          const int T = part.t1 - part.t0;
-          ok = wait(qr, seg, kSiteQFull);
-#pragma unroll 1
-          for (int j = 0; ok && j < T; ++j) {
-            const int gi = done + j, st = gi % C::NT, u = gi & 1;
-            ok = wait(&kr[st], gi / C::NT, kSiteKFull);
-            // the buffer's weights have been multiplied
-            if (ok && gi >= 2) ok = wait(&sh.v_empty[(gi - 2) % C::NT], (gi - 2) / C::NT, kSiteSFull);
+      while (ok && tree_next(p, kBN, walk, part)) {
+        const int T = part.t1 - part.t0;
+        if constexpr (NQ == 2) {
+          // A query tile's products, then its next scores into the place of its
+          // weights, while the other one's scores are exponentiated.
+#pragma unroll
+          for (int tile = 0; tile < 2; ++tile) {
+            if (ok && (Q8 || tile == 0)) ok = all_wait(q_there(tile), seg, kSiteQFull);
+            if (ok && tile == 0) ok = all_wait(k_there(done), done / C::NT, kSiteKFull);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t at = st * C::TILE;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const int a = k / (C::ATOM / 16), w = k % (C::ATOM / 16);
-              tc_mma_ss<PAIR>(tmem + u * kBN, dq.at(a * C::QBOX + w * 32), dk.at(at + a * C::KBOX + w * 32), idesc,
-                              k > 0 ? 1u : 0u);
-            }
-            tc_commit<PAIR>(&sh.s_full[u]);
-            tc_commit<PAIR>(&sh.k_empty[st]);
+            scores(done, tile, tile);
           }
-          if (ok) tc_commit<PAIR>(&sh.q_empty);  // the part's last scores
-          done += T;
-          ++seg;
-        }
-        // every product finishes before TMEM is released
-        tc_commit<PAIR>(&sh.drain[0]);
-        tc_drain(&sh.drain[0], 0, wd);
-      }
-      // (the second CTA: the last of the arrivals that reach into it)
-      if (PAIR && rank == 1 && lane == 0) tc_drain(&sh.drain[0], 0, wd);
-      __syncwarp();
-    } else if (warp == C::ISSUE_PV) {
-      // ---------------------------------------------------------- P V (the pair's first CTA)
-      if (rank == 0 && lane == 0) {
-        const uint32_t idesc = idesc_bf16_f32(128 * C::CTAS, D, false, true) & ~C::FORMAT;
-        const Desc dv(smem_u32(smem + C::OFF_V), C::VBOX, C::SBOV, C::SWZV);
-        const uint32_t t_o = tmem + C::TM_O;
-#pragma unroll 1
-        while (ok && tree_next(p, kBN, walk, part)) {
-          const int T = part.t1 - part.t0;
-          if (seg > 0) ok = wait(&sh.o_free, seg - 1, kSiteOFull);  // the previous part's O has been read
+          if (ok && T == 1) commit(&sh.q_empty);
 #pragma unroll 1
           for (int j = 0; ok && j < T; ++j) {
-            const int gi = done + j, st = gi % C::NT, u = gi & 1;
-            ok = wait(&sh.v_ready[st], gi / C::NT, kSiteVFull);
-            const uint32_t at = st * C::TILE;
+            const int gi = done + j;
+            const bool more = j + 1 < T;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (ok) ok = wait(&sh.p_full[u][half], gi >> 1, kSitePFull);
+            for (int tile = 0; tile < 2; ++tile) {
+              // (the previous part's O has been read)
+              if (j == 0 && seg > 0) ok = all_wait(&sh.o_free[tile], seg - 1, kSiteOFull);
+              if (ok && tile == 0)
+                ok = lane & 1      ? wait(v_there(gi), gi / C::NT, kSiteVFull)
+                     : more && lane & 2 ? wait(k_there(gi + 1), (gi + 1) / C::NT, kSiteKFull)
+                                   : wait(&sh.p_full[tile][0], gi, kSitePFull);
+              else if (ok) ok = wait(&sh.p_full[tile][0], gi, kSitePFull);
+              ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < kBN / 32; ++k)
-                tc_mma_ts<PAIR>(t_o, tmem + u * kBN + half * 32 + k * 8,
-                                dv.at(at + (half * 4 + k) * 16 * C::ATOMV * 2), idesc,
-                                (j > 0 || half > 0 || k > 0) ? 1u : 0u);
+              products(gi, tile, tile, 0, kBN / 16, j == 0);
+              if (more) scores(gi + 1, tile, tile);
+              else commit(&sh.o_full[tile]);
             }
-            if (ok) tc_commit<PAIR>(&sh.v_empty[st]);
+            if (ok && j + 2 == T) commit(&sh.q_empty);  // the part's last scores
           }
-          done += T;
-          ++seg;
+        } else if (who == 0) {
+          ok = all_wait(q_there(0), seg, kSiteQFull);
+#pragma unroll 1
+          for (int j = 0; ok && j < T; ++j) {
+            const int gi = done + j;
+            // (the buffer's weights have been multiplied)
+            ok = gi >= 2 ? wait_both(k_there(gi), gi / C::NT, &sh.v_empty[(gi - 2) % C::NT], (gi - 2) / C::NT, kSiteKFull)
+                         : all_wait(k_there(gi), gi / C::NT, kSiteKFull);
+            if (!ok) break;
+            tc_fence_after();
+            scores(gi, 0, gi & 1);
+          }
+          if (ok) commit(&sh.q_empty);
+        } else {
+          if (seg > 0) ok = all_wait(&sh.o_free[0], seg - 1, kSiteOFull);
+#pragma unroll 1
+          for (int j = 0; ok && j < T; ++j) {
+            const int gi = done + j, u = gi & 1;
+            ok = wait_both(v_there(gi), gi / C::NT, &sh.p_full[u][0], gi >> 1, kSitePFull);
+            if (!ok) break;
+            tc_fence_after();
+            products(gi, 0, u, 0, kBN / 32, j == 0);
+            ok = all_wait(&sh.p_full[u][1], gi >> 1, kSitePFull);
+            if (!ok) break;
+            tc_fence_after();
+            products(gi, 0, u, kBN / 32, kBN / 16, j == 0);
+          }
+          if (ok) commit(&sh.o_full[0]);
         }
-        tc_commit<PAIR>(&sh.drain[1]);
-        tc_drain(&sh.drain[1], 0, wd);
+        done += T;
+        ++seg;
       }
-      if (PAIR && rank == 1 && lane == 0) tc_drain(&sh.drain[1], 0, wd);
+      // every product finishes before TMEM is released
+      commit(&sh.drain[who]);
+      }
+      // (the second CTA: the last of the arrivals that reach into it)
+      tc_drain(&sh.drain[who], 0, wd);
       __syncwarp();
     } else if (!Q8 && warp == C::CLEANER) {
       // ---------------------------------------------------------- cleaner of V tiles
@@ -857,7 +930,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (PAIR) {
           ok = __all_sync(0xffffffffu, wait(&sh.q_full, seg, kSiteQFull));
           if (!ok) break;
-          tell_issuer<PAIR>(&sh.q_ready);
+          tell_issuer<PAIR>(&sh.q_ready[0]);
         }
 #pragma unroll 1
         for (int j = 0; j < T; ++j) {
@@ -903,23 +976,23 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   tc_fence_before();
   __syncthreads();
   if (PAIR) cluster_sync();  // nothing reaches into the other CTA any more
-  if (warp == C::ISSUE_S) {
+  if (warp == C::ISSUE) {
     tc_fence_after();
     tc_dealloc<PAIR>(tmem);
   }
 }
 
-template <int D, bool PAIR, bool Q8>
+template <int D, bool PAIR, int NQ, bool Q8>
 cudaError_t launch_tc(int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const TreeParams& p, cudaStream_t stream) {
-  using C = Tc<D, PAIR, Q8>;
+  using C = Tc<D, PAIR, NQ, Q8>;
   static std::atomic<int> ready[64];  // 1: usable, 2: the register split does not fit the compiled kernel
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   int state = ready[dev & 63].load(std::memory_order_relaxed);
   if (state == 0) {
-    e = cudaFuncSetAttribute(attn_tree_tc_kernel<D, PAIR, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_tree_tc_kernel<D, PAIR, NQ, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
     state = 1;
@@ -927,7 +1000,7 @@ cudaError_t launch_tc(int grid, int least, const CUtensorMap& tq, const CUtensor
       // setmaxnreg.inc waits until registers are free: the shares must fit in
       // what the CTA is launched with, or the kernel would never proceed
       cudaFuncAttributes fa;
-      if ((e = cudaFuncGetAttributes(&fa, attn_tree_tc_kernel<D, PAIR, Q8>)) != cudaSuccess) return e;
+      if ((e = cudaFuncGetAttributes(&fa, attn_tree_tc_kernel<D, PAIR, NQ, Q8>)) != cudaSuccess) return e;
       if (fa.numRegs * C::THREADS < C::R_SUM) state = 2;
     }
     ready[dev & 63].store(state, std::memory_order_relaxed);
@@ -945,31 +1018,39 @@ cudaError_t launch_tc(int grid, int least, const CUtensorMap& tq, const CUtensor
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   prof_begin(kKindTree, stream);
-  e = cudaLaunchKernelEx(&cfg, attn_tree_tc_kernel<D, PAIR, Q8>, tq, tk, tv, p, least);
+  e = cudaLaunchKernelEx(&cfg, attn_tree_tc_kernel<D, PAIR, NQ, Q8>, tq, tk, tv, p, least);
   prof_end(kKindTree, stream);
   return e;
 }
 
+template <int D, bool PAIR, int NQ>
+cudaError_t launch_tc_of(bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
+  return quantised ? launch_tc<D, PAIR, NQ, true>(grid, least, tq, tk, tv, p, stream)
+                   : launch_tc<D, PAIR, NQ, false>(grid, least, tq, tk, tv, p, stream);
+}
+
+template <int D>
+cudaError_t launch_tc_d(bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
+  switch (p.block_rows) {
+    case 128: return launch_tc_of<D, false, 1>(quantised, grid, least, tq, tk, tv, p, stream);
+    case 256: return launch_tc_of<D, true, 1>(quantised, grid, least, tq, tk, tv, p, stream);
+    case 512: return launch_tc_of<D, true, 2>(quantised, grid, least, tq, tk, tv, p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 }  // namespace
 
-cudaError_t launch_tree_tc(int d, bool pair, bool quantised, int grid, int least, const CUtensorMap& tq,
-                           const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
-  if (d == 32)
-    return quantised ? launch_tc<32, false, true>(grid, least, tq, tk, tv, p, stream)
-                     : launch_tc<32, false, false>(grid, least, tq, tk, tv, p, stream);
-  if (d == 64 && !pair)
-    return quantised ? launch_tc<64, false, true>(grid, least, tq, tk, tv, p, stream)
-                     : launch_tc<64, false, false>(grid, least, tq, tk, tv, p, stream);
-  if (d == 64)
-    return quantised ? launch_tc<64, true, true>(grid, least, tq, tk, tv, p, stream)
-                     : launch_tc<64, true, false>(grid, least, tq, tk, tv, p, stream);
-  if (d == 128 && !pair)
-    return quantised ? launch_tc<128, false, true>(grid, least, tq, tk, tv, p, stream)
-                     : launch_tc<128, false, false>(grid, least, tq, tk, tv, p, stream);
-  if (d == 128)
-    return quantised ? launch_tc<128, true, true>(grid, least, tq, tk, tv, p, stream)
-                     : launch_tc<128, true, false>(grid, least, tq, tk, tv, p, stream);
-  return cudaErrorInvalidValue;
+cudaError_t launch_tree_tc(int d, bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
+                           const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
+  switch (d) {
+    case 32: return launch_tc_of<32, false, 1>(quantised, grid, least, tq, tk, tv, p, stream);
+    case 64: return launch_tc_d<64>(quantised, grid, least, tq, tk, tv, p, stream);
+    case 128: return launch_tc_d<128>(quantised, grid, least, tq, tk, tv, p, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace attn

@@ -494,7 +494,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (idle) {
           tc_fence_before();
           tell_issuer<PAIR>(&sh.p_full[u][0]);
-          if (NQ == 1) tell_issuer<PAIR>(&sh.p_full[u][1]);
+          tell_issuer<PAIR>(&sh.p_full[u][1]);
           continue;
         }
         uint32_t s[4][32];
@@ -512,42 +512,16 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               if (!((seen >> i) & 1u)) s[q][i] = __float_as_uint(-INFINITY);
           }
         }
-        float mx[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) mx[v] = fmaxf(__uint_as_float(s[0][2 * v]), __uint_as_float(s[0][2 * v + 1]));
-#pragma unroll
-        for (int e = 8; e < kBN; e += 8)
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            mx[v] = max3(mx[v], __uint_as_float(s[(e + 2 * v) >> 5][(e + 2 * v) & 31]),
-                         __uint_as_float(s[(e + 2 * v + 1) >> 5][(e + 2 * v + 1) & 31]));
-        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        float alpha = 1.f;
-        bool moved = false;
-        if (j == 0) {
-          m_used = m_new;
-        } else if (m_new > m_used + kGrow) {
-          alpha = ex2_approx(m_used - m_new);  // from -inf: 0
-          m_used = m_new;
-          moved = true;
-        }
-        const float m_ref = m_used == -INFINITY ? 0.f : m_used - kLow;  // nothing seen yet: weights 0
-        const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
-        if (j > 0 && __any_sync(0xffffffffu, moved)) {
-          // the products so far are in O (two query tiles: the scores came after
-          // them; the scores of one, a buffer ahead, do not show that)
-          if (NQ == 1) {
-            ok = __all_sync(0xffffffffu, wait(&sh.v_empty[(gi - 1) % C::NT], (gi - 1) / C::NT, kSitePFull));
-            if (!ok) break;
-            tc_fence_after();
-          }
-          tc_rescale<D>(t_o, alpha);
-          l *= alpha;
-        }
-        // weights of 64 keys, then of the other 64, whose products start meanwhile
-        uint64_t acc0 = f2_pack(l, 0.f), acc1 = f2_pack(0.f, 0.f);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        // Weights of 64 keys, against the reference so far; if the tile's maximum,
+        // found meanwhile, is too far above it, again against that one. Then the
+        // other 64, while the products with the first are under way.
+        uint64_t acc0, acc1, nm2;
+        auto refer = [&]() {
+          const float m_ref = m_used == -INFINITY ? 0.f : m_used - kLow;  // nothing seen yet: weights 0
+          nm2 = f2_pack(-m_ref, -m_ref);
+          acc0 = acc1 = f2_pack(0.f, 0.f);
+        };
+        auto weights = [&](int half) {
 #pragma unroll
           for (int q = 2 * half; q < 2 * half + 2; ++q) {
             uint32_t pk[16];
@@ -564,15 +538,49 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             tmem_st16(t_s + q * 16, pk);
           }
-          if (NQ == 2 && half == 0) continue;  // (the issuer is with the other query tile)
+        };
+        refer();
+        weights(0);
+        float mx[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) mx[v] = fmaxf(__uint_as_float(s[0][2 * v]), __uint_as_float(s[0][2 * v + 1]));
+#pragma unroll
+        for (int e = 8; e < kBN; e += 8)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            mx[v] = max3(mx[v], __uint_as_float(s[(e + 2 * v) >> 5][(e + 2 * v) & 31]),
+                         __uint_as_float(s[(e + 2 * v + 1) >> 5][(e + 2 * v + 1) & 31]));
+        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool moved = m_new > m_used + kGrow;
+        tmem_st_wait();
+        if (__any_sync(0xffffffffu, moved)) {
+          const float alpha = moved ? ex2_approx(m_used - m_new) : 1.f;  // from -inf: 0
+          if (moved) m_used = m_new;
+          if (j > 0) {
+            // the products so far are in O (two query tiles: the scores came after
+            // them; the scores of one, a buffer ahead, do not show that)
+            if (NQ == 1) {
+              ok = __all_sync(0xffffffffu, wait(&sh.v_empty[(gi - 1) % C::NT], (gi - 1) / C::NT, kSitePFull));
+              if (!ok) break;
+              tc_fence_after();
+            }
+            tc_rescale<D>(t_o, alpha);
+            l *= alpha;
+          }
+          refer();
+          weights(0);
           tmem_st_wait();
-          tc_fence_before();
-          tell_issuer<PAIR>(&sh.p_full[u][NQ == 1 ? half : 0]);
         }
+        tc_fence_before();
+        tell_issuer<PAIR>(&sh.p_full[u][0]);
+        weights(1);
+        tmem_st_wait();
+        tc_fence_before();
+        tell_issuer<PAIR>(&sh.p_full[u][1]);
         float a0, a1, a2, a3;
         f2_unpack(acc0, a0, a1);
         f2_unpack(acc1, a2, a3);
-        l = (a0 + a1) + (a2 + a3);
+        l += (a0 + a1) + (a2 + a3);
       }
       // the last tile's product
       done += T;
@@ -878,7 +886,11 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc_fence_after();
-              products(gi, tile, tile, 0, kBN / 16, j == 0);
+              products(gi, tile, tile, 0, kBN / 32, j == 0);
+              ok = all_wait(&sh.p_full[tile][1], gi, kSitePFull);
+              if (!ok) break;
+              tc_fence_after();
+              products(gi, tile, tile, kBN / 32, kBN / 16, j == 0);
               if (more) scores(gi + 1, tile, tile);
               else commit(&sh.o_full[tile]);
             }

@@ -94,14 +94,17 @@ def test_every_row_count(n):
 
 
 @pytest.mark.parametrize("quantised", [False, True])
-@pytest.mark.parametrize("n,group,d", [(6, 1, 64), (40, 4, 128), (64, 1, 32)])
-def test_what_a_query_does_not_see_never_reaches_it(n, group, d, quantised):
+@pytest.mark.parametrize("n,group,d,hkv,m", [
+    (6, 1, 64, 1, 150), (40, 4, 128, 1, 150), (64, 1, 32, 1, 150),
+    # batches large enough for tiles of 128 query rows, pairs of them, pairs of two
+    (64, 2, 32, 32, 2300), (40, 4, 128, 24, 1200), (64, 8, 64, 8, 1100), (64, 8, 128, 8, 1100)])
+def test_what_a_query_does_not_see_never_reaches_it(n, group, d, hkv, m, quantised):
     """NaN and infinities behind the sequence and in drafted positions: queries that see them
     get NaN or infinities, the others the finite result; words of 0 are rows that see the
     text alone, or nothing."""
-    B, m, lens = 3, 150, [150 - 30, 100, n]
-    q = R.bf16(B, group, n, d, seed=1)
-    c, (k, v) = caches(B, 1, m, d, quantised, 5)
+    B, lens = 3, [m - 30, m - 50, n]
+    q = R.bf16(B, hkv * group, n, d, seed=1)
+    c, (k, v) = caches(B, hkv, m, d, quantised, 5)
     words = R.random_tree(B, n, 9)
     words[0][n - 1] = words[2][n - 1] = words[2][0] = 0
     for b in range(B):
@@ -116,15 +119,15 @@ def test_what_a_query_does_not_see_never_reaches_it(n, group, d, quantised):
     bad = [1, 3]  # drafted tokens whose key (the first) and value (the second) are not finite
     for b in range(B):
         if quantised:
-            c[0].view(torch.uint8)[b, 0, lens[b] - n + bad[0], d // 2] = 0x7f
-            c[1].view(torch.uint8)[b, 0, lens[b] - n + bad[1], 3] = 0x7f
+            c[0].view(torch.uint8)[b, :, lens[b] - n + bad[0], d // 2] = 0x7f
+            c[1].view(torch.uint8)[b, :, lens[b] - n + bad[1], 3] = 0x7f
         else:
-            c[0][b, 0, lens[b] - n + bad[0], d // 2] = float("nan")
-            c[1][b, 0, lens[b] - n + bad[1], 3] = float("inf")
+            c[0][b, :, lens[b] - n + bad[0], d // 2] = float("nan")
+            c[1][b, :, lens[b] - n + bad[1], 3] = float("inf")
     o, lse = run(q, c, lens, words, d ** -0.5)
     ref = list(R.tree_step(q, k, v, lens, words, d ** -0.5))
-    hit = torch.tensor([[[bool(w >> bad[0] & 1) for w in r]] * group for r in words])
-    val = torch.tensor([[[bool(w >> bad[1] & 1) for w in r]] * group for r in words])
+    hit = torch.tensor([[[bool(w >> bad[0] & 1) for w in r]] * (hkv * group) for r in words])
+    val = torch.tensor([[[bool(w >> bad[1] & 1) for w in r]] * (hkv * group) for r in words])
     o, lse = o.cpu(), lse.cpu()
     assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
     col = o[..., 3]
@@ -139,6 +142,46 @@ def test_what_a_query_does_not_see_never_reaches_it(n, group, d, quantised):
     o2[..., 3] = torch.where(val, 0.0, o2[..., 3].float()).bfloat16()
     ref_o[..., 3] = torch.where(val, 0.0, ref_o[..., 3])
     R.check_tree(o2[sel], lse[sel], [x[sel] for x in (ref_o, ref[1], ref[2], ref[3])])
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("n", [17, 31, 33, 48, 63, 64])
+def test_row_counts_in_large_batches(n, d):
+    """Rows around the edges of large query tiles, lengths around the key tiles' edges."""
+    B, hkv, m = 16, 8, 1600
+    lens = [n, 127 + n, 129, 256, 1600, 1599, 1025, 0, 1, 128, 1537, 1000, 1600, 640, 641, 639]
+    words = R.random_tree(B, n, n)
+    for quantised, group in ((False, 1), (True, 3), (False, 5), (True, 8)):
+        q = R.bf16(B, hkv * group, n, d, seed=n)
+        c, (k, v) = caches(B, hkv, m, d, quantised, n + 100)
+        o, lse = run(q, c, lens, words, d ** -0.5)
+        for b in range(B):
+            g = b % hkv
+            hs = slice(g * group, (g + 1) * group)
+            ref = R.tree_step(q[b:b + 1, hs], k[b:b + 1, g:g + 1], v[b:b + 1, g:g + 1], [lens[b]], [words[b]], d ** -0.5)
+            R.check_tree(o[b:b + 1, hs], lse[b:b + 1, hs], ref)
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_grow_along_the_cache(d, quantised):
+    """A running maximum that has to move many times: keys longer from tile to tile, and back."""
+    B, hkv, group, n, m = 4, 8, 8, 40, 2000
+    q = R.bf16(B, hkv * group, n, d, seed=1)
+    c, (k, v) = caches(B, hkv, m, d, False, 3)
+    size = (1 + 40 * torch.sin(torch.arange(m) / 300.0).abs())[:, None]
+    k = (k.float() * size).bfloat16()
+    if quantised:
+        (kc, ke), (vc, ve) = R.quantise(k), R.quantise(v)
+        k, v = (x * torch.exp2(e.double() - 127)[..., None] for x, e in ((kc, ke), (vc, ve)))
+        c = (kc.float().to(E4M3).to(DEV), vc.float().to(E4M3).to(DEV), ke.to(DEV), ve.to(DEV))
+    else:
+        c = (k.to(DEV), v.to(DEV), None, None)
+    o, lse = run(q, c, None, None, d ** -0.5)
+    for b in range(B):
+        hs = slice(b * group, (b + 1) * group)
+        ref = R.tree_step(q[b:b + 1, hs], k[b:b + 1, b:b + 1], v[b:b + 1, b:b + 1], [m], None, d ** -0.5)
+        R.check_tree(o[b:b + 1, hs], lse[b:b + 1, hs], ref)
 
 
 def test_causal_words_equal_no_words_and_plain_decoding():

@@ -704,10 +704,19 @@ int small_ctas(int d, bool quantised) {
   }
 }
 
-bool tree_uses_tc(int rows, int d, bool quantised) {
-  (void)d;
-  (void)quantised;
-  return rows > 32;
+// Which kernel: the mma.sync one multiplies with the keys of a tile once for every
+// 16 rows, the tcgen05 one once for 128. Taking what the first needs for 16 rows and
+// 128 keys as 1, the second was measured at `tile` for 128 keys, `start` for each
+// unit it begins (e4m3: its scales are looked at first) and, where the whole step is
+// so small that latency counts, `fill` more in all. (mma.sync : tcgen05 in us; 16
+// sequences of 8192 positions, 4 key heads of d = 128, bf16: 16 rows 80 : 93, 32 rows
+// 161 : 93; e4m3: 32 rows 91 : 105, 48 rows 134 : 106; 64 sequences of 1024, 64 rows,
+// bf16 178 : 81, e4m3 111 : 111; 2 of 2000, 64 rows, bf16 19 : 21, 96 rows 23 : 22.)
+bool tree_uses_tc(long long heads, int rows, int m, int d, bool quantised) {
+  const double tile = d == 32 ? 3.0 : d == 64 ? (quantised ? 2.5 : 1.5) : (quantised ? 2.0 : 1.0);
+  const double start = quantised ? 24.0 : 8.0, fill = d == 32 ? 2400.0 : 600.0;
+  const double tiles = (m + 127) / 128, small = (rows + kTreeRows - 1) / kTreeRows, big = (rows + 127) / 128;
+  return static_cast<double>(heads) * (small * tiles - big * (tile * tiles + start)) > fill;
 }
 
 template <int D, bool Q8, bool HALF>
@@ -764,7 +773,7 @@ cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMa
 
 TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised) {
   TreePlan l{};
-  l.tc = tree_uses_tc(rows, d, quantised);
+  l.tc = tree_uses_tc(static_cast<long long>(B) * h_kv, rows, m, d, quantised);
   if (l.tc) {
     l.pair = rows > 128 && d >= 64;
     l.block_rows = !l.pair ? 128 : rows > 256 ? 512 : 256;

@@ -354,7 +354,7 @@ TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised);
 cudaError_t launch_tree(int d, bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
                         const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
 // The tcgen05 kernel (attn_tree_tc.cu).
-cudaError_t launch_tree_tc(int d, bool quantised, int grid, int least, const CUtensorMap& tq,
+cudaError_t launch_tree_tc(int d, bool quantised, int grid, const CUtensorMap& tq,
                            const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream);
 
 }  // namespace attn

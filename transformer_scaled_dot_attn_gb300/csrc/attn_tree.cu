@@ -31,13 +31,17 @@ using namespace sm103;
 constexpr int kTreeWarps = 4;
 constexpr int kTreeThreads = kTreeWarps * 32;
 constexpr int kTreeRows = 16;     // query rows of a CTA (one mma.sync tile)
-constexpr int kTreeLeast = 2;     // tiles (of four warps) worth a CTA of their own
-constexpr int kTreeLeastTc = 2;   // the same for the tcgen05 kernel
 // Tiles' worth of time that beginning a unit takes. With 0, 1, 2, 3, 4: 73.0, 71.4,
-// 69.3, 69.0, 70.3 us (64 sequences of uneven lengths, 16 heads of one row, e4m3), 98.7 to
+// 69.3, 69.0, 70.3 us (64 sequences of uneven lengths, 16 heads of one row, e4m3); 98.7 to
 // 96.4 us from 2 on (4 sequences, 512 rows, e4m3).
 constexpr int kTreeLead = 3;
-constexpr int kTreeShort = 8;     // tiles of a cache that one CTA takes alone
+// A CTA takes a unit alone, and nothing has to be joined, where it does not have to do
+// more than this many tiles above an equal share for that. (Alone : shared, us: one
+// sequence of 300 positions, 8 heads of 5 rows, d = 64: 5.9 : 8.1; 2 of 1000, e4m3: 11.9 :
+// 9.8; 16 of 1500, 8 key heads of 128 rows, d = 128: 29.3 : 38.2; 8 of 2000, 4 key heads,
+// e4m3: 31.2 : 23.1.) And in caches of at most so many tiles only, as the lengths may differ.
+constexpr double kTreeShort = 7.5;
+constexpr int kTreeAlone = 16, kTreeAloneMany = 8;  // (more units than places on the GPU)
 
 template <int D, bool Q8>
 struct Tree {
@@ -230,7 +234,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const Watchdog wd = p.wd;
   grid_launch_dependents();
   TreeWalk walk;
-  if (!tree_start(p, C::BN, kTreeLeast, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), walk)) return;
+  if (!tree_start(p, C::BN, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), walk)) return;
   if (tid == 0) {
     for (int w = 0; w < kTreeWarps; ++w)
       for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[w][s], 1);
@@ -615,8 +619,8 @@ __device__ __forceinline__ UnitParts unit_parts(const TreeParams& p, const TreeL
 
 // Grid: x = unit, y = 8 rows of its block (a warp a row).
 template <int D>
-__global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p, int bn, int grid, int least) {
-  const TreeLine l = tree_line(p, bn, grid, least);
+__global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p, int bn, int grid) {
+  const TreeLine l = tree_line(p, bn, grid);
   const int unit = blockIdx.x, lane = threadIdx.x & 31;
   const UnitParts u = unit_parts(p, l, unit, bn);
   grid_wait();  // the parts are written
@@ -652,8 +656,8 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p
 
 // Grid: x = unit, y = 32 rows of its block (a lane a row); each of the 8 warps D / 8 columns.
 template <int D>
-__global__ void __launch_bounds__(256) attn_tree_tc_merge_kernel(const TreeParams p, int bn, int grid, int least) {
-  const TreeLine l = tree_line(p, bn, grid, least);
+__global__ void __launch_bounds__(256) attn_tree_tc_merge_kernel(const TreeParams p, int bn, int grid) {
+  const TreeLine l = tree_line(p, bn, grid);
   const int unit = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const UnitParts u = unit_parts(p, l, unit, bn);
   grid_wait();
@@ -751,7 +755,7 @@ template <int D>
 cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tk,
                           const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   cudaError_t e;
-  if (plan.tc) e = launch_tree_tc(D, quantised, plan.grid, kTreeLeastTc, tq, tk, tv, p, stream);
+  if (plan.tc) e = launch_tree_tc(D, quantised, plan.grid, tq, tk, tv, p, stream);
   else if (quantised) e = launch_small_rows<D, true>(plan.grid, tk, tv, p, stream);
   else e = launch_small_rows<D, false>(plan.grid, tk, tv, p, stream);
   if (e != cudaSuccess || plan.by_unit) return e;
@@ -759,11 +763,11 @@ cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMa
   prof_begin(kKindTreeMerge, stream);
   if (plan.tc) {
     e = launch_dependent(attn_tree_tc_merge_kernel<D>, dim3(units, static_cast<unsigned>(p.block_rows / 32)), dim3(256),
-                         stream, p, plan.tile, plan.grid, kTreeLeastTc);
+                         stream, p, plan.tile, plan.grid);
   } else {
     const int warps = p.block_rows < 8 ? p.block_rows : 8;
     e = launch_dependent(attn_tree_merge_kernel<D>, dim3(units, static_cast<unsigned>((p.block_rows + 7) / 8)),
-                         dim3(static_cast<unsigned>(warps * 32)), stream, p, plan.tile, plan.grid, kTreeLeast);
+                         dim3(static_cast<unsigned>(warps * 32)), stream, p, plan.tile, plan.grid);
   }
   prof_end(kKindTreeMerge, stream);
   return e;
@@ -786,17 +790,17 @@ TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised) {
   const long long units = static_cast<long long>(B) * h_kv * l.row_blocks;
   const long long tiles = (m + l.tile - 1) / l.tile;
   const long long room = l.tc ? kSms / (l.pair ? 2 : 1) : kSms * small_ctas(d, quantised);
-  // Short caches: a CTA for each unit, nothing to join. Else one CTA for each
-  // place (or pair of places) on the GPU's SMs; fewer where the caches hold too few tiles.
-  l.by_unit = tiles <= kTreeShort && (units <= room || (!l.tc && units <= 0x7fffffffLL));
+  // Short caches: a CTA for each unit. Else one CTA for each place (or pair of
+  // places) on the GPU's SMs; fewer where the caches hold too few tiles.
+  l.by_unit = units <= room
+                  ? tiles <= kTreeAlone && static_cast<double>(tiles) * (room - units) <= kTreeShort * room
+                  : !l.tc && tiles <= kTreeAloneMany && units <= 0x7fffffffLL;
   if (l.by_unit) {
     l.grid = static_cast<int>(units);
   } else {
-    const int least = l.tc ? kTreeLeastTc : kTreeLeast;
     l.lead = kTreeLead;
-    const long long most = (units * (tiles + l.lead) + least - 1) / least;
+    const long long most = (units * (tiles + l.lead) + kTreeLeast - 1) / kTreeLeast;
     l.grid = static_cast<int>(most < room ? most : room);
-    if (l.grid == 1) l.by_unit = true;  // one tile of one unit
   }
   l.slots = units + l.grid;
   return l;

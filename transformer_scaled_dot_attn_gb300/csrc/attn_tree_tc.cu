@@ -1,20 +1,28 @@
 // Decoding of drafted tokens with many query rows a key head (attn_tree.cu
 // states the operator): tcgen05 tiles of 128 query rows against 128 keys.
 //
-// A CTA holds one tile of 128 rows and walks its share of the line of tiles
-// (attn_tree.cuh). Where a key head has more than 128 rows, two CTAs of a cluster
-// work as a pair on 256 (cta_group::2): each holds its 128 rows of Q, S, P and O
-// but only half of every K tile (64 keys) and V tile (half of the columns), so
-// the pair reads, converts and keeps each K/V tile once. The first CTA's issuer
-// feeds both SMs' tensor cores; what it waits for, both CTAs report to it.
+// A CTA walks its share of the line of tiles (attn_tree.cuh) with
+//   128 rows: one query tile;
+//   256 rows: two CTAs of a cluster as a pair (cta_group::2): each holds its 128
+//     rows of Q, S, P and O but only half of every K tile (64 keys) and V tile (half
+//     of the columns), so the pair reads, converts and keeps each K/V tile once.
+//     The first CTA's issuers feed both SMs' tensor cores; what they wait for,
+//     both CTAs report to them;
+//   512 rows: a pair with two query tiles in each CTA, which take turns: while one
+//     tile's scores are exponentiated, the tensor cores have the other's products.
+// Bound by that exchange. 4 sequences of 20480 positions, 4 key heads of 512 rows,
+// d = 128: 75 us over bf16 caches, 81 over e4m3 (the products alone need 44.5 at
+// the rate of a large matrix product); a pair with one tile took 81 and 96. A turn
+// of the two tiles takes some 2800 clocks, 2180 of them products, and a share of
+// 34 turns starts with 10 us of first loads and set-up.
 //   producer    TMA loads. bf16 caches: K and V into their rings in the tensor
 //               cores' layout. e4m3 caches: the codes into rings of their own.
-//   converters  (e4m3; 4 warps for K, 4 for V) write f16 values into the K and V
-//               rings, code 2^(e - top + 7) with `top` the largest scale of the
-//               part's keys: so a code is converted once for all rows, one
-//               conversion and one exact product for two codes, and the softmax
-//               carries no scales. f16 holds them exactly down to 2^-22 of the
-//               largest; below that they lose low bits, and 2^-33 becomes 0.
+//   converters  (e4m3; 4 warps, for one query tile 4 for K and 4 for V) write f16
+//               values into the K and V rings, code 2^(e - top + 7) with `top` the
+//               largest scale of the part's keys: so a code is converted once for all
+//               rows, one conversion and one exact product for two codes, and the
+//               softmax carries no scales. f16 holds them exactly down to 2^-22 of
+//               the largest; below that they lose low bits, and 2^-33 becomes 0.
 //               The queries are brought to f16 as well, each row to [2^14, 2^15)
 //               by a power of two, and the weights are f16 against a reference
 //               2^7 below the maximum, so that they reach down to 2^-31 of it.
@@ -23,14 +31,17 @@
 //               are not finite (weight 0 times NaN is NaN). Rows that see such a
 //               value get it added at the end. (The converters do this for e4m3.)
 //               In a pair it reports Q and K tiles as well.
-//   issuers     one thread for S = Q K^T into one of two S buffers, one for
-//               O += P V: a thread that waits, computes descriptors and commits
-//               between its products takes about as long for a tile's S or P V as
-//               the products themselves (one thread for both: 2900 clocks a tile).
-//   softmax     one thread a row: x = S c, running maximum (O rescaled when it
-//               grew by more than 2^8), p = 2^(x - m), P over S in TMEM, 64 keys
+//   issuers     one query tile: a warp for S = Q K^T into one of two S buffers, one
+//               for O += P V. Two: one warp, products of a tile's weights and then its
+//               next scores into their place; with a warp for each tile both tiles
+//               ran in step and the tensor cores stood still between (102 us for 75).
+//               A warp's lanes look at the barriers it waits for at once: a wait for
+//               one that is ready takes 150 clocks.
+//   softmax     one thread a row: x = S c, p = 2^(x - m), P over S in TMEM, 64 keys
 //               at a time so that their products start while the other 64 are
-//               exponentiated.
+//               exponentiated. The reference m is the one so far; the tile's maximum is
+//               sought meanwhile, and only if it is more than 2^8 above it the weights
+//               are taken again and O is rescaled (maximum first: 87 us, this way 81).
 // A waiter must not be overtaken: a wait tells a barrier's phases apart by their
 // parity alone, so every phase that is waited for needs the waiter's own doing
 // before the next one can complete. (So K and V have rings of their own: the
@@ -372,7 +383,7 @@ __device__ __forceinline__ void mark_odd(TcShared& sh, int seg, uint32_t rank) {
 template <int D, bool PAIR, int NQ, bool Q8>
 __global__ void __launch_bounds__(Tc<D, PAIR, NQ, Q8>::THREADS, 1)
 attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const TreeParams p, int least) {
+                    const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
   using C = Tc<D, PAIR, NQ, Q8>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) TcShared sh;
@@ -384,7 +395,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   const Watchdog wd = p.wd;
   grid_launch_dependents();
   TreeWalk walk;
-  if (!tree_start(p, kBN, least, static_cast<int>(blockIdx.x) / C::CTAS, static_cast<int>(gridDim.x) / C::CTAS, walk))
+  if (!tree_start(p, kBN, static_cast<int>(blockIdx.x) / C::CTAS, static_cast<int>(gridDim.x) / C::CTAS, walk))
     return;  // (both CTAs of a pair, or neither)
   if (warp == C::PRODUCER) {
     // (a lane a place of the rings)
@@ -995,7 +1006,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 }
 
 template <int D, bool PAIR, int NQ, bool Q8>
-cudaError_t launch_tc(int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_tc(int grid, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                       const TreeParams& p, cudaStream_t stream) {
   using C = Tc<D, PAIR, NQ, Q8>;
   static std::atomic<int> ready[64];  // 1: usable, 2: the register split does not fit the compiled kernel
@@ -1030,37 +1041,37 @@ cudaError_t launch_tc(int grid, int least, const CUtensorMap& tq, const CUtensor
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   prof_begin(kKindTree, stream);
-  e = cudaLaunchKernelEx(&cfg, attn_tree_tc_kernel<D, PAIR, NQ, Q8>, tq, tk, tv, p, least);
+  e = cudaLaunchKernelEx(&cfg, attn_tree_tc_kernel<D, PAIR, NQ, Q8>, tq, tk, tv, p);
   prof_end(kKindTree, stream);
   return e;
 }
 
 template <int D, bool PAIR, int NQ>
-cudaError_t launch_tc_of(bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
+cudaError_t launch_tc_of(bool quantised, int grid, const CUtensorMap& tq, const CUtensorMap& tk,
                          const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
-  return quantised ? launch_tc<D, PAIR, NQ, true>(grid, least, tq, tk, tv, p, stream)
-                   : launch_tc<D, PAIR, NQ, false>(grid, least, tq, tk, tv, p, stream);
+  return quantised ? launch_tc<D, PAIR, NQ, true>(grid, tq, tk, tv, p, stream)
+                   : launch_tc<D, PAIR, NQ, false>(grid, tq, tk, tv, p, stream);
 }
 
 template <int D>
-cudaError_t launch_tc_d(bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
+cudaError_t launch_tc_d(bool quantised, int grid, const CUtensorMap& tq, const CUtensorMap& tk,
                         const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   switch (p.block_rows) {
-    case 128: return launch_tc_of<D, false, 1>(quantised, grid, least, tq, tk, tv, p, stream);
-    case 256: return launch_tc_of<D, true, 1>(quantised, grid, least, tq, tk, tv, p, stream);
-    case 512: return launch_tc_of<D, true, 2>(quantised, grid, least, tq, tk, tv, p, stream);
+    case 128: return launch_tc_of<D, false, 1>(quantised, grid, tq, tk, tv, p, stream);
+    case 256: return launch_tc_of<D, true, 1>(quantised, grid, tq, tk, tv, p, stream);
+    case 512: return launch_tc_of<D, true, 2>(quantised, grid, tq, tk, tv, p, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_tree_tc(int d, bool quantised, int grid, int least, const CUtensorMap& tq, const CUtensorMap& tk,
+cudaError_t launch_tree_tc(int d, bool quantised, int grid, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   switch (d) {
-    case 32: return launch_tc_of<32, false, 1>(quantised, grid, least, tq, tk, tv, p, stream);
-    case 64: return launch_tc_d<64>(quantised, grid, least, tq, tk, tv, p, stream);
-    case 128: return launch_tc_d<128>(quantised, grid, least, tq, tk, tv, p, stream);
+    case 32: return launch_tc_of<32, false, 1>(quantised, grid, tq, tk, tv, p, stream);
+    case 64: return launch_tc_d<64>(quantised, grid, tq, tk, tv, p, stream);
+    case 128: return launch_tc_d<128>(quantised, grid, tq, tk, tv, p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -616,69 +616,98 @@ def attn_bwd_noalloc(q, k, v, o, lse, dO, causal: bool = False, scale: Optional[
     return dq, dk, dv
 
 
-def _operand(name, t, shape, dtype, device):
-    """Checks one tensor of the calls below and returns its address (None for None)."""
+# (These calls are made once or several times for every layer of a decoding step, so
+# a check that passes costs as little as it can; what a check objects to is found out
+# afterwards. torch and two of its functions are looked up once.)
+_torch = _raw_stream = _current_device = None
+
+
+def _lookup():
+    global _torch, _raw_stream, _current_device
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    # (the handle without a Stream object)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = torch.cuda.current_device
+    _torch = torch
+    return torch
 
 
-def _first(name, t, dims, dtype):
-    """The tensor that gives a call its sizes and its device."""
+def _refuse(name, t, shape, dtype, device):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
-    _operand(name, t, t.shape, dtype, t.device)
-    return t.device
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _operand(name, t, shape, dtype, device):
+    """Checks one tensor of the calls below and returns its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(name, t, shape, dtype, device)
+
+
+def _first(name, t, dims, dtype):
+    """Checks the tensor that gives a call its sizes; returns its device and shape."""
+    try:
+        device, shape = t.device, t.shape
+        if t.is_cuda and t.dtype is dtype and len(shape) == dims and t.is_contiguous():
+            return device, shape
+    except AttributeError:
+        device, shape = None, ()
+    if len(shape) != dims and device is not None and t.is_cuda:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(shape)}")
+    _refuse(name, t, shape, dtype, device)
 
 
 def _workspace(t, need, device):
-    import torch
+    """Address and size of a call's workspace, which is allocated where it was not given."""
+    torch = _torch or _lookup()
     if t is None:
-        t = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if need == 0:
+            return None, None, 0
+        t = torch.empty(need, dtype=torch.uint8, device=device)
     elif not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return t, t.numel() * t.element_size()
+    return t, t.data_ptr(), t.numel() * t.element_size()
 
 
 def _launch(fn, where, device, stream, *args):
     """Calls fn(*args, stream) with the tensors' device current; raises on a status."""
-    import torch
+    torch = _torch or _lookup()
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = _raw_stream(index)
     elif stream.device != device:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream.cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    if _current_device() == index:
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, handle)
     if st != ATTN_OK:
         raise AttnError(st, where)
 
 
 def _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections):
     """Sizes, addresses and sections shared by attn_qk_norm_rope and its backward."""
-    import torch
+    torch = _torch or _lookup()
     bf = torch.bfloat16
     first = k if q is None else q
-    dev = _first("k" if q is None else "q", first, 4, bf)
-    B, h, n, d = first.shape
+    dev, (B, h, n, d) = _first("k" if q is None else "q", first, 4, bf)
     h_kv = 0 if k is None else int(k.shape[1]) if k.dim() == 4 else -1
     if q is None:
         h = 0
@@ -716,7 +745,7 @@ def attn_qk_norm_rope(q, k, w_q, w_k, positions=None, freqs=None, sections=None,
     columns (i, i + len(freqs)), or neighbours with ``interleaved``. Without freqs: the
     norm alone. q or k (with its weight) may be None. q_out may be q, k_out may be k.
     Returns (q_out, k_out)."""
-    import torch
+    torch = _torch or _lookup()
     dev, (B, h, h_kv, n, d, rot, axes, sec), ptrs = _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections)
     if q is not None and q_out is None:
         q_out = torch.empty_like(q)
@@ -724,8 +753,9 @@ def attn_qk_norm_rope(q, k, w_q, w_k, positions=None, freqs=None, sections=None,
         k_out = torch.empty_like(k)
     po = None if q is None else _operand("q_out", q_out, q.shape, torch.bfloat16, dev)
     ko = None if k is None else _operand("k_out", k_out, k.shape, torch.bfloat16, dev)
-    _launch(load_library().attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, *ptrs, po, ko, B, h, h_kv, n, d, rot,
-            axes, sec, 1 if interleaved else 0, eps)
+    lib = _lib or load_library()
+    _launch(lib.attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, *ptrs, po, ko, B, h, h_kv, n, d, rot, axes, sec,
+            1 if interleaved else 0, eps)
     return q_out, k_out
 
 
@@ -738,7 +768,7 @@ def attn_qk_norm_rope_bwd(q, k, w_q, w_k, positions, freqs, dq_out, dk_out, sect
     """Gradients of attn_qk_norm_rope from those of its results (dq_out, dk_out, e.g. of
     attn_bwd); the other arguments as in the forward. dq may be dq_out, dk may be dk_out.
     Returns (dq, dk, dw_q, dw_k)."""
-    import torch
+    torch = _torch or _lookup()
     bf = torch.bfloat16
     dev, (B, h, h_kv, n, d, rot, axes, sec), ptrs = _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections)
     up, out, dws = [], [], []
@@ -752,21 +782,21 @@ def attn_qk_norm_rope_bwd(q, k, w_q, w_k, positions, freqs, dq_out, dk_out, sect
         up.append(None if x is None else _operand(f"d{name}_out", g, x.shape, bf, dev))
         out.append(None if x is None else _operand(f"d{name}", dx, x.shape, bf, dev))
         dws.append(None if x is None else _operand(f"dw_{name}", dw, (d,), bf, dev))
-    lib = load_library()
+    lib = _lib or load_library()
     need = 0 if workspace is not None else lib.attn_qk_norm_rope_bwd_workspace_bytes(B, h, h_kv, n, d)
-    workspace, ws_bytes = _workspace(workspace, need, dev)
+    workspace, ws, ws_bytes = _workspace(workspace, need, dev)
     _launch(lib.attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream, *ptrs, *up, *out, *dws, B, h, h_kv, n, d,
-            rot, axes, sec, 1 if interleaved else 0, eps, workspace.data_ptr(), ws_bytes)
+            rot, axes, sec, 1 if interleaved else 0, eps, ws, ws_bytes)
     return dq, dk, dw_q, dw_k
 
 
 def _cache_args(k_cache, v_cache, k_exp, v_exp):
     """Device, sizes and addresses of a cache: bf16, or e4m3 codes with exponent bytes."""
-    import torch
+    torch = _torch or _lookup()
     dtype = torch.bfloat16 if k_exp is None else torch.float8_e4m3fn
-    dev = _first("k cache", k_cache, 4, dtype)
-    B, h_kv, m, d = k_cache.shape
-    v = _operand("v cache", v_cache, k_cache.shape, dtype, dev)
+    dev, shape = _first("k cache", k_cache, 4, dtype)
+    B, h_kv, m, d = shape
+    v = _operand("v cache", v_cache, shape, dtype, dev)
     if k_exp is None:
         if v_exp is not None:
             raise ValueError("k_exp and v_exp go together")
@@ -783,7 +813,7 @@ def attn_cache_write(k, v, k_cache, v_cache, kv_len=None, new_len=None, k_exp=No
     k_exp, v_exp (uint8 [B, h_kv, m]) the caches are torch.float8_e4m3fn and the rows are
     quantised as they are written; without, the caches are bf16. Everything else in the
     caches stays as it was. Returns (k_cache, v_cache)."""
-    import torch
+    torch = _torch or _lookup()
     dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k_cache, v_cache, k_exp, v_exp)
     if k.dim() != 4:
         raise ValueError("k, v must be [B, h_kv, n, d]")
@@ -792,15 +822,15 @@ def attn_cache_write(k, v, k_cache, v_cache, kv_len=None, new_len=None, k_exp=No
     pv = _operand("v", v, (B, h_kv, n, d), torch.bfloat16, dev)
     lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
     new = None if new_len is None else _operand("new_len", new_len, (B,), torch.int32, dev)
-    _launch(load_library().attn_cache_write, "attn_cache_write", dev, stream, pk, pv, kc, vc, ke, ve, lens, new, B,
-            h_kv, n, m, d)
+    lib = _lib or load_library()
+    _launch(lib.attn_cache_write, "attn_cache_write", dev, stream, pk, pv, kc, vc, ke, ve, lens, new, B, h_kv, n, m, d)
     return k_cache, v_cache
 
 
 def attn_cache_read(k_cache, v_cache, k_exp, v_exp, kv_len=None, k=None, v=None, stream=None):
     """A quantised cache (attn_cache_write) back as bf16 k, v [B, h_kv, m, d], exactly; rows
     at or past kv_len (int32 CUDA [B], default m) are zeros. Returns (k, v)."""
-    import torch
+    torch = _torch or _lookup()
     if k_exp is None:
         raise ValueError("attn_cache_read takes a quantised cache: k_exp and v_exp are needed")
     dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k_cache, v_cache, k_exp, v_exp)
@@ -809,8 +839,8 @@ def attn_cache_read(k_cache, v_cache, k_exp, v_exp, kv_len=None, k=None, v=None,
     pk = _operand("k", k, k_cache.shape, torch.bfloat16, dev)
     pv = _operand("v", v, k_cache.shape, torch.bfloat16, dev)
     lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
-    _launch(load_library().attn_cache_read, "attn_cache_read", dev, stream, kc, vc, ke, ve, pk, pv, lens, B, h_kv, m,
-            d)
+    lib = _lib or load_library()
+    _launch(lib.attn_cache_read, "attn_cache_read", dev, stream, kc, vc, ke, ve, pk, pv, lens, B, h_kv, m, d)
     return k, v
 
 
@@ -828,7 +858,7 @@ def attn_decode_tree(q, k, v, kv_len=None, tree=None, k_exp=None, v_exp=None, sc
     before L - n, and position L - n + t where bit t of tree[b, i] (int64 CUDA [B, n]) is
     set; without tree where t <= i. A query that sees nothing gives O = 0, lse = -inf.
     Returns (O, lse)."""
-    import torch
+    torch = _torch or _lookup()
     bf = torch.bfloat16
     dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k, v, k_exp, v_exp)
     if q.dim() != 4:
@@ -842,9 +872,9 @@ def attn_decode_tree(q, k, v, kv_len=None, tree=None, k_exp=None, v_exp=None, sc
     if need_lse and lse is None:
         lse = torch.empty((B, h, n), dtype=torch.float32, device=dev)
     pl = None if lse is None else _operand("lse", lse, (B, h, n), torch.float32, dev)
-    lib = load_library()
+    lib = _lib or load_library()
     need = 0 if workspace is not None else lib.attn_decode_tree_workspace_bytes(B, h, h_kv, n, m, d)
-    workspace, ws_bytes = _workspace(workspace, need, dev)
+    workspace, ws, ws_bytes = _workspace(workspace, need, dev)
     _launch(lib.attn_decode_tree, "attn_decode_tree", dev, stream, pq, kc, vc, po, pl, ke, ve, lens, words, B, h, h_kv,
-            n, m, d, 1.0 / math.sqrt(d) if scale is None else float(scale), workspace.data_ptr(), ws_bytes)
+            n, m, d, 1.0 / math.sqrt(d) if scale is None else float(scale), ws, ws_bytes)
     return out, lse

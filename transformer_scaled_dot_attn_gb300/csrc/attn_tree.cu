@@ -36,10 +36,10 @@ constexpr int kTreeRows = 16;     // query rows of a CTA (one mma.sync tile)
 // 96.4 us from 2 on (4 sequences, 512 rows, e4m3).
 constexpr int kTreeLead = 3;
 // A CTA takes a unit alone, and nothing has to be joined, where it does not have to do
-// more than this many tiles above an equal share for that. (Alone : shared, us: one
+// more than this many 128 keys above an equal share for that. (Alone : shared, us: one
 // sequence of 300 positions, 8 heads of 5 rows, d = 64: 5.9 : 8.1; 2 of 1000, e4m3: 11.9 :
 // 9.8; 16 of 1500, 8 key heads of 128 rows, d = 128: 29.3 : 38.2; 8 of 2000, 4 key heads,
-// e4m3: 31.2 : 23.1.) And in caches of at most so many tiles only, as the lengths may differ.
+// e4m3: 31.2 : 23.1.) And in caches of at most so many 128 only, as the lengths may differ.
 constexpr double kTreeShort = 7.5;
 constexpr int kTreeAlone = 16, kTreeAloneMany = 8;  // (more units than places on the GPU)
 
@@ -213,15 +213,50 @@ __device__ __forceinline__ void value_words(const uint8_t* tile, int r, int g, u
   }
 }
 
+// The four warps' results, `sall` [warp][row][D + 4], as a part's or the final result.
+template <int D, int ROWS>
+__device__ __forceinline__ void tree_join(const TreeParams& p, const TreePart& part, const float* sall,
+                                          const float (&s_m)[kTreeWarps][ROWS], const float (&s_l)[kTreeWarps][ROWS],
+                                          int row0) {
+  constexpr int OST = D + 4, TPR = kTreeThreads / ROWS;  // pitch; threads of an output row
+  const int tid = threadIdx.x, r = tid / TPR, row = row0 + r;
+  if (row >= p.rows) return;
+  float M = -INFINITY, sum = 0.f, f[kTreeWarps];
+#pragma unroll
+  for (int w = 0; w < kTreeWarps; ++w) M = fmaxf(M, s_m[w][r]);
+#pragma unroll
+  for (int w = 0; w < kTreeWarps; ++w) {
+    f[w] = M == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - M);
+    sum = fmaf(f[w], s_l[w][r], sum);
+  }
+  auto joined = [&](int col) {
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kTreeWarps; ++w) o = fmaf(f[w], sall[(w * ROWS + r) * OST + col], o);
+    return o;
+  };
+  if (part.whole) {
+    const float inv = M == -INFINITY ? 0.f : 1.f / sum;  // a row that saw no key is the empty sum
+    const size_t out = static_cast<size_t>(part.bh) * p.rows + row;
+    for (int col = (tid % TPR) * 2; col < D; col += TPR * 2)
+      *reinterpret_cast<uint32_t*>(p.o + out * D + col) = pack_bf16x2(joined(col) * inv, joined(col + 1) * inv);
+    if (tid % TPR == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
+  } else {
+    const size_t at = static_cast<size_t>(part.slot) * p.block_rows + r;
+    for (int col = (tid % TPR) * 2; col < D; col += TPR * 2)
+      *reinterpret_cast<float2*>(p.part + at * D + col) = make_float2(joined(col), joined(col + 1));
+    if (tid % TPR == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(M, sum);
+  }
+}
+
 // One CTA per share of the line of tiles (attn_tree.cuh); a tile is the four
-// warps' TK keys each. HALF: at most 8 query rows, so that rows 8 to 15 of the
-// products are left out of the softmax.
-template <int D, bool Q8, bool HALF>
+// warps' TK keys each.
+template <int D, bool Q8>
 __global__ void __launch_bounds__(kTreeThreads, Tree<D, Q8>::CTAS)
 attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const TreeParams p) {
   using C = Tree<D, Q8>;
-  constexpr int H = HALF ? 1 : 2;  // halves of the 16 rows in use: a thread's rows are g and g + 8
+  constexpr int H = 2;  // a thread's rows: g and g + 8
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kTreeWarps][C::STAGES];
   __shared__ int abort_word;
@@ -274,12 +309,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     float c[H];  // per row: |scale| log2(e), and for e4m3 the inverse of the row's power of two
     unsigned long long word[H];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h >= H) {
-#pragma unroll
-        for (int s = 0; s < C::KS; ++s) qa[s][1] = qa[s][3] = 0u;
-        break;
-      }
+    for (int h = 0; h < H; ++h) {
       const int row = min(row0 + g + 8 * h, p.rows - 1);
       const __nv_bfloat16* q = p.q + (static_cast<size_t>(bh) * p.rows + row) * D;
       const uint32_t sign = p.c < 0.f ? 0x80008000u : 0u;
@@ -551,37 +581,375 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       }
     }
     __syncthreads();
-    const float* sall = reinterpret_cast<const float*>(smem);
-    constexpr int TPR = kTreeThreads / (8 * H);  // threads of an output row
-    const int r = tid / TPR, row = row0 + r;
-    if (row < p.rows) {
-      float M = -INFINITY, sum = 0.f, f[kTreeWarps];
-#pragma unroll
-      for (int w = 0; w < kTreeWarps; ++w) M = fmaxf(M, s_m[w][r]);
-#pragma unroll
-      for (int w = 0; w < kTreeWarps; ++w) {
-        f[w] = M == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - M);
-        sum = fmaf(f[w], s_l[w][r], sum);
+    tree_join<D, kTreeRows>(p, part, reinterpret_cast<const float*>(smem), s_m, s_l, row0);
+    turn += mine;
+    fence_proxy_async_smem();  // the results in the ring come before the next part's TMA writes
+    __syncthreads();
+  }
+}
+
+// At most 8 query rows a key head (decoding of one token, mostly): the products
+// the other way round, 16 keys (or 16 output columns) against 8 query rows, so that
+// no part of a product is idle. Half as many products as above and half the
+// registers for O; the weights are turned from (key, row) to (row, key) by an
+// 8 x 8 transposition in registers. Bound by reading the caches. (64 sequences of up
+// to 4096 positions, 16 heads of one row, d = 64, e4m3: 64 us, 69 with the kernel
+// above, reading alone 51; 32 such of bf16: 83, 90, 79. d = 32, e4m3: 57 us with 64 keys
+// a warp's tile, 65 with 32; d = 64: 64 with either.)
+template <int D, bool Q8>
+struct Few : Tree<D, Q8> {
+  using T = Tree<D, Q8>;
+  static constexpr int CTAS = D == 128 ? 2 : Q8 ? 4 : 5;   // per SM
+  static constexpr int TK = Q8 && D == 32 ? 64 : T::TK;    // keys per tile of a warp
+  static constexpr uint32_t KT = TK * D * T::ES;           // one K (or V) tile
+  static constexpr int BN = kTreeWarps * TK;               // keys of a CTA's tile
+  static constexpr int NG = TK / 16;                       // groups of 16 keys in a warp's tile
+  static constexpr int NB = Q8 ? TK / 32 : 1;              // scale bytes of a lane
+  static constexpr int ND = D / 16;                        // groups of 16 output columns
+  static constexpr uint32_t RING = kTreeWarps * T::STAGES * 2 * KT;
+  static constexpr uint32_t JOIN = kTreeWarps * 8 * T::OST * 4;
+  static constexpr uint32_t SMEM = (RING > JOIN ? RING : JOIN) + 1024;
+};
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(kTreeThreads, Few<D, Q8>::CTAS)
+attn_tree_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const TreeParams p) {
+  using C = Few<D, Q8>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kTreeWarps][C::STAGES];
+  __shared__ int abort_word;
+  __shared__ float s_m[kTreeWarps][8], s_l[kTreeWarps][8];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  volatile int* abort_flag = &abort_word;
+  const Watchdog wd = p.wd;
+  grid_launch_dependents();
+  TreeWalk walk;
+  if (!tree_start(p, C::BN, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), walk)) return;
+  if (tid == 0) {
+    for (int w = 0; w < kTreeWarps; ++w)
+      for (int s = 0; s < C::STAGES; ++s) mbar_init(&full[w][s], 1);
+    abort_word = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  __syncthreads();
+  uint8_t* ring = smem + warp * (C::STAGES * 2 * C::KT);
+  int turn = 0;  // tiles this warp has put through its ring
+  TreePart part;
+#pragma unroll 1
+  while (tree_next(p, C::BN, walk, part)) {
+    const int bh = part.bh, L = part.L;
+    const int old = L - p.n;             // positions before the newest n (negative: fewer cached than n)
+    const int mine = part.t1 - part.t0;  // of every tile this warp takes keys [warp TK, warp TK + TK)
+    const int key0 = part.t0 * C::BN + warp * C::TK;
+    auto load = [&](int x) {
+      const int st = (turn + x) % C::STAGES;
+      const int k0 = key0 + x * C::BN;
+      uint8_t* dst = ring + st * 2 * C::KT;
+      mbar_arrive_expect_tx(&full[warp][st], 2 * C::KT);
+      for (int a = 0; a < C::NBOX; ++a) {
+        tma_load_3d(dst + a * C::BOX, &tm_k, &full[warp][st], a * (C::ROWB / C::ES), k0, bh);
+        tma_load_3d(dst + C::KT + a * C::BOX, &tm_v, &full[warp][st], a * (C::ROWB / C::ES), k0, bh);
       }
-      auto joined = [&](int col) {
-        float o = 0.f;
+    };
+    if (lane == 0)
+      for (int x = 0; x < C::STAGES && x < mine; ++x) load(x);
+
+    // Row g of the queries as the B operand, in the types and scales of the kernel
+    // above. What the softmax needs of a row, the threads of rows 2t, 2t + 1 have.
+    uint32_t qb[C::KS][2];
+    float c[2];
+    unsigned long long word[2];
+    {
+      const __nv_bfloat16* q = p.q + (static_cast<size_t>(bh) * p.rows + min(g, p.rows - 1)) * D;
+      const uint32_t sign = p.c < 0.f ? 0x80008000u : 0u;
+      float mine_c = fmaxf(fabsf(p.c), 1e-30f);  // (scale 0: 0 times the -inf of a masked score would be NaN)
+      if constexpr (Q8) {
+        uint32_t top = 0;
 #pragma unroll
-        for (int w = 0; w < kTreeWarps; ++w) o = fmaf(f[w], sall[(w * kTreeRows + r) * C::OST + col], o);
-        return o;
-      };
-      if (part.whole) {
-        const float inv = M == -INFINITY ? 0.f : 1.f / sum;  // a row that saw no key is the empty sum
-        const size_t out = static_cast<size_t>(bh) * p.rows + row;
-        for (int col = (tid % TPR) * 2; col < D; col += TPR * 2)
-          *reinterpret_cast<uint32_t*>(p.o + out * D + col) = pack_bf16x2(joined(col) * inv, joined(col + 1) * inv);
-        if (tid % TPR == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
+        for (int s = 0; s < C::KS; ++s) {
+          const int at = D == 128 ? 16 * (t + 4 * (s >> 2)) + 4 * (s & 3) : D == 64 ? 16 * t + 4 * s : 8 * t + 4 * s;
+          const uint2 u = *reinterpret_cast<const uint2*>(q + at);
+          qb[s][0] = u.x ^ sign;
+          qb[s][1] = u.y ^ sign;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t lo = qb[s][e] & 0x7fffu, hi = (qb[s][e] >> 16) & 0x7fffu;
+            top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+          }
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t up = 268u - max(top >> 7, 15u);
+        const float f = __uint_as_float(up << 23);
+        mine_c = fmaxf(mine_c * __uint_as_float((254u - up) << 23), 1e-37f);
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = unpack_bf16x2(qb[s][e]);
+            qb[s][e] = pack_f16x2(x.x * f, x.y * f);
+          }
       } else {
-        const size_t at = static_cast<size_t>(part.slot) * p.block_rows + r;
-        for (int col = (tid % TPR) * 2; col < D; col += TPR * 2)
-          *reinterpret_cast<float2*>(p.part + at * D + col) = make_float2(joined(col), joined(col + 1));
-        if (tid % TPR == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(M, sum);
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s) {
+          qb[s][0] = *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t) ^ sign;
+          qb[s][1] = *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * t) ^ sign;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        c[h] = __shfl_sync(0xffffffffu, mine_c, 4 * (2 * t + h));
+        word[h] = tree_word(p, part.b, min(2 * t + h, p.rows - 1));
       }
     }
+    // this thread's keys within a group of 16 scores: kg, kg + 8; within 16 of V: ka, kb, ka + 8, kb + 8
+    const int kg = Q8 ? key_of<D>(g) : g;
+    const int ka = Q8 ? key_of<D>(2 * t) : 2 * t, kb = Q8 ? key_of<D>(2 * t + 1) : 2 * t + 1;
+
+    float acc[C::ND][4];  // columns (two), rows 2t and 2t + 1
+#pragma unroll
+    for (int i = 0; i < C::ND; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: this thread's keys only
+
+    // e4m3: the scale bytes as above, of keys j, j + 32
+    int ke[C::NB], ve[C::NB], top_v = 0;
+    auto scales = [&](int x) {
+#pragma unroll
+      for (int u = 0; u < C::NB; ++u) {
+        const int key = key0 + x * C::BN + u * 32 + lane;
+        const bool in = x < mine && key < L;
+        const size_t at = static_cast<size_t>(bh) * p.m + key;
+        ke[u] = in ? __ldg(p.k_exp + at) : 0;
+        ve[u] = in ? __ldg(p.v_exp + at) : 0;
+      }
+    };
+    if constexpr (Q8) scales(0);
+
+    int x = 0;
+    for (; x < mine; ++x) {
+      const int st = (turn + x) % C::STAGES;
+      const int k0 = key0 + x * C::BN;
+      const uint8_t* sk = ring + st * 2 * C::KT;
+      const uint8_t* sv = sk + C::KT;
+      const uint32_t ak = smem_u32(sk), av = smem_u32(sv);
+      float fk[C::NB], fv[C::NB], back = 1.f;
+      if constexpr (Q8) {
+        int top = ve[0];
+#pragma unroll
+        for (int u = 1; u < C::NB; ++u) top = max(top, ve[u]);
+        top = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(top)));
+        if (top > top_v) {
+          back = ex2_approx(static_cast<float>(top_v - top));  // (an empty product before the first: any factor)
+          top_v = top;
+        }
+#pragma unroll
+        for (int u = 0; u < C::NB; ++u) {
+          fk[u] = pow2_of_byte(ke[u]);
+          const int e = ve[u] - top_v + 127 + 15;
+          fv[u] = e > 0 ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 0.f;
+        }
+        scales(x + 1);
+      }
+      if (!__all_sync(0xffffffffu, tree_wait(&full[warp][st], ((turn + x) / C::STAGES) & 1, abort_flag, wd))) break;
+
+      // scores of the tile's keys
+      float s[C::NG][4];
+#pragma unroll
+      for (int i = 0; i < C::NG; ++i) {
+        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        if constexpr (Q8) {
+          uint32_t w0[C::KS], w1[C::KS];
+          key_words<D>(sk, i * 16 + kg, t, w0);
+          key_words<D>(sk, i * 16 + 8 + kg, t, w1);
+#pragma unroll
+          for (int k = 0; k < C::KS; ++k) {
+            const uint32_t a[4] = {e4m3_to_f16x2(w0[k] & 0xffffu), e4m3_to_f16x2(w1[k] & 0xffffu),
+                                   e4m3_to_f16x2(w0[k] >> 16), e4m3_to_f16x2(w1[k] >> 16)};
+            mma_f16(s[i], a, qb[k][0], qb[k][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < C::KS; ++k) {
+            uint32_t a[4];
+            ldsm4(ak + tile_off<D, false>(i * 16 + (lane & 15), (2 * k + (lane >> 4)) * 16), a);
+            mma_bf16(s[i], a, qb[k][0], qb[k][1]);
+          }
+        }
+      }
+      // the keys' scales, and the mask where the tile reaches past the positions that every row sees
+      const bool tail = k0 + C::TK > old;
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < C::NG; ++i) {
+        if constexpr (Q8) {
+          const float f0 = __shfl_sync(0xffffffffu, fk[i / 2], (i & 1) * 16 + kg);
+          const float f1 = __shfl_sync(0xffffffffu, fk[i / 2], (i & 1) * 16 + 8 + kg);
+          s[i][0] *= f0, s[i][1] *= f0, s[i][2] *= f1, s[i][3] *= f1;
+        }
+        if (tail) {
+          const int j = k0 + i * 16 + kg;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!sees(word[h], j, old, L)) s[i][h] = -INFINITY;
+            if (!sees(word[h], j + 8, old, L)) s[i][2 + h] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) top[h] = fmaxf(top[h], fmaxf(s[i][h], s[i][2 + h]));
+      }
+      bool grew = Q8 && back != 1.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
+        top[h] *= c[h];  // in units of log2
+        grew |= top[h] > m[h];
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float n = fmaxf(m[h], top[h]);
+          const float f = ex2_approx(m[h] - (n == -INFINITY ? 0.f : n));
+          m[h] = n;
+          l[h] *= f;
+#pragma unroll
+          for (int i = 0; i < C::ND; ++i) {
+            acc[i][h] *= f * back;
+            acc[i][2 + h] *= f * back;
+          }
+        }
+      }
+      float ref[2];  // nothing seen yet: weights 0
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ref[h] = m[h] == -INFINITY ? 0.f : m[h];
+
+      // weights (rounded as above) and V^T P^T, 16 keys at a time
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < C::NG; ++i) {
+        float f0 = 1.f, f1 = 1.f, w[4];
+        if constexpr (Q8) {
+          f0 = __shfl_sync(0xffffffffu, fv[i / 2], (i & 1) * 16 + kg);
+          f1 = __shfl_sync(0xffffffffu, fv[i / 2], (i & 1) * 16 + 8 + kg);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[h] = ex2_approx(fmaf(s[i][h], c[h], -ref[h]));
+          w[2 + h] = ex2_approx(fmaf(s[i][2 + h], c[h], -ref[h]));
+          l[h] += w[h] + w[2 + h];
+        }
+        const uint32_t p0 = transposed(Q8 ? pack_f16x2(w[0] * f0, w[1] * f0) : pack_bf16x2(w[0], w[1]));
+        const uint32_t p1 = transposed(Q8 ? pack_f16x2(w[2] * f1, w[3] * f1) : pack_bf16x2(w[2], w[3]));
+        if constexpr (Q8) {
+          constexpr int W = D / 32;  // words of this thread's columns in a row
+          uint32_t v[4][W];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) value_words<D>(sv, i * 16 + (u >> 1) * 8 + ((u & 1) ? kb : ka), g, v[u]);
+          if (tail) {
+            // NaN codes may not enter a product here: a weight of 0 would make
+            // them NaN for rows that do not see them
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int j = 0; j < W; ++j) {
+                const uint32_t n = nan_codes(v[u][j]) & 0x80808080u;
+                if (n != 0) {
+                  odd = true;
+                  v[u][j] &= ~((n >> 7) * 0xffu);
+                }
+              }
+          }
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            // codes of the keys of columns 2t, 2t + 1 side by side, then of 2t + 8, 2t + 9
+            const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5140), a1 = __byte_perm(v[0][j], v[1][j], 0x7362);
+            const uint32_t b0 = __byte_perm(v[2][j], v[3][j], 0x5140), b1 = __byte_perm(v[2][j], v[3][j], 0x7362);
+            const uint32_t lo[4] = {e4m3_to_f16x2(a0 & 0xffffu), e4m3_to_f16x2(a0 >> 16), e4m3_to_f16x2(b0 & 0xffffu),
+                                    e4m3_to_f16x2(b0 >> 16)};
+            const uint32_t hi[4] = {e4m3_to_f16x2(a1 & 0xffffu), e4m3_to_f16x2(a1 >> 16), e4m3_to_f16x2(b1 & 0xffffu),
+                                    e4m3_to_f16x2(b1 >> 16)};
+            mma_f16(acc[2 * j], lo, p0, p1);
+            mma_f16(acc[2 * j + 1], hi, p0, p1);
+          }
+        } else {
+          const int base = k0 + i * 16;
+          const bool ra = base + ka < L, rb = base + kb < L, rc = base + 8 + ka < L, rd = base + 8 + kb < L;
+#pragma unroll
+          for (int j = 0; j < C::ND; ++j) {
+            uint32_t v[4];
+            ldsm4_t(av + tile_off<D, false>(i * 16 + (lane & 7) + 8 * (lane >> 4), (2 * j + ((lane >> 3) & 1)) * 16), v);
+            if (tail) {
+              v[0] = clean_pair(v[0], ra, rb, odd);
+              v[1] = clean_pair(v[1], ra, rb, odd);
+              v[2] = clean_pair(v[2], rc, rd, odd);
+              v[3] = clean_pair(v[3], rc, rd, odd);
+            }
+            mma_bf16(acc[j], v, p0, p1);
+          }
+        }
+      }
+      // column of acc[i][2 e + h]
+      auto column = [&](int i, int e) { return Q8 ? col_of<D>(g) * (D / 8) + 2 * i + e : i * 16 + g + 8 * e; };
+      if (tail && __any_sync(0xffffffffu, odd)) {
+        // values left out above that are not finite: only for the rows that see them
+#pragma unroll 1
+        for (int j = 0; j < C::TK; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (sees(word[h], k0 + j, old, L))
+#pragma unroll
+              for (int i = 0; i < C::ND; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float v = value_at<D, Q8>(sv, j, column(i, e));
+                  if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) acc[i][2 * e + h] += v;
+                }
+      }
+      __syncwarp();
+      if (lane == 0 && x + C::STAGES < mine) {
+        fence_proxy_async_smem();  // the warp's reads of the stage come before the TMA write
+        load(x + C::STAGES);
+      }
+    }
+    if (x < mine && lane == 0)  // the watchdog fired: let the tiles in flight land
+      for (int y = x; y < x + C::STAGES && y < mine; ++y)
+        tree_drain(&full[warp][(turn + y) % C::STAGES], ((turn + y) / C::STAGES) & 1, wd);
+    // join the four warps' results; every load has landed
+    if (__syncthreads_or(x < mine)) return;
+    float* so = reinterpret_cast<float*>(smem) + warp * (8 * C::OST);
+    const float unit_v = Q8 ? pow2_of_byte(top_v) * 0x1p-15f : 1.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+      // a row whose every score was NaN has no maximum: its sum is NaN, against the reference 0
+      if (m[h] == -INFINITY && l[h] != 0.f) m[h] = 0.f;
+#pragma unroll
+      for (int i = 0; i < C::ND; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = Q8 ? col_of<D>(g) * (D / 8) + 2 * i + e : i * 16 + g + 8 * e;
+          so[(2 * t + h) * C::OST + col] = acc[i][2 * e + h] * unit_v;
+        }
+      if (g == 0) {
+        s_m[warp][2 * t + h] = m[h];
+        s_l[warp][2 * t + h] = l[h];
+      }
+    }
+    __syncthreads();
+    tree_join<D, 8>(p, part, reinterpret_cast<const float*>(smem), s_m, s_l, 0);
     turn += mine;
     fence_proxy_async_smem();  // the results in the ring come before the next part's TMA writes
     __syncthreads();
@@ -700,11 +1068,19 @@ __global__ void __launch_bounds__(256) attn_tree_tc_merge_kernel(const TreeParam
   if (warp == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
 }
 
-int small_ctas(int d, bool quantised) {
+// Places of the mma.sync kernels on the GPU, and keys of a CTA's tile.
+template <int D, bool Q8>
+void small_shape_of(bool few, int* places, int* tile) {
+  *places = kSms * (few ? Few<D, Q8>::CTAS : Tree<D, Q8>::CTAS);
+  *tile = few ? Few<D, Q8>::BN : Tree<D, Q8>::BN;
+}
+
+void small_shape(int d, bool quantised, bool few, int* places, int* tile) {
   switch (d) {
-    case 32: return quantised ? Tree<32, true>::CTAS : Tree<32, false>::CTAS;
-    case 64: return quantised ? Tree<64, true>::CTAS : Tree<64, false>::CTAS;
-    default: return quantised ? Tree<128, true>::CTAS : Tree<128, false>::CTAS;
+    case 32: return quantised ? small_shape_of<32, true>(few, places, tile) : small_shape_of<32, false>(few, places, tile);
+    case 64: return quantised ? small_shape_of<64, true>(few, places, tile) : small_shape_of<64, false>(few, places, tile);
+    default:
+      return quantised ? small_shape_of<128, true>(few, places, tile) : small_shape_of<128, false>(few, places, tile);
   }
 }
 
@@ -723,22 +1099,22 @@ bool tree_uses_tc(long long heads, int rows, int m, int d, bool quantised) {
   return static_cast<double>(heads) * (small * tiles - big * (tile * tiles + start)) > fill;
 }
 
-template <int D, bool Q8, bool HALF>
+template <int D, bool Q8, bool FEW>
 cudaError_t launch_small(int grid, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                          cudaStream_t stream) {
-  using C = Tree<D, Q8>;
+  constexpr auto kernel = FEW ? attn_tree_few_kernel<D, Q8> : attn_tree_kernel<D, Q8>;
+  constexpr uint32_t smem = FEW ? Few<D, Q8>::SMEM : Tree<D, Q8>::SMEM;
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!set[dev & 63].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(attn_tree_kernel<D, Q8, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(C::SMEM));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     set[dev & 63].store(true, std::memory_order_relaxed);
   }
   prof_begin(kKindTree, stream);
-  attn_tree_kernel<D, Q8, HALF><<<static_cast<unsigned>(grid), kTreeThreads, C::SMEM, stream>>>(tk, tv, p);
+  kernel<<<static_cast<unsigned>(grid), kTreeThreads, smem, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   prof_end(kKindTree, stream);
   return e;
@@ -778,23 +1154,25 @@ cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMa
 TreePlan tree_plan(int B, int h_kv, int rows, int m, int d, bool quantised) {
   TreePlan l{};
   l.tc = tree_uses_tc(static_cast<long long>(B) * h_kv, rows, m, d, quantised);
+  int room;
   if (l.tc) {
     l.pair = rows > 128 && d >= 64;
     l.block_rows = !l.pair ? 128 : rows > 256 ? 512 : 256;
     l.tile = 128;
+    room = kSms / (l.pair ? 2 : 1);
   } else {
     l.block_rows = rows < kTreeRows ? rows : kTreeRows;
-    l.tile = kTreeWarps * ((d == 128 && !quantised) ? 16 : 32);
+    small_shape(d, quantised, rows <= 8, &room, &l.tile);
   }
   l.row_blocks = (rows + l.block_rows - 1) / l.block_rows;
   const long long units = static_cast<long long>(B) * h_kv * l.row_blocks;
   const long long tiles = (m + l.tile - 1) / l.tile;
-  const long long room = l.tc ? kSms / (l.pair ? 2 : 1) : kSms * small_ctas(d, quantised);
   // Short caches: a CTA for each unit. Else one CTA for each place (or pair of
   // places) on the GPU's SMs; fewer where the caches hold too few tiles.
+  const long long blocks = (m + 127) / 128;
   l.by_unit = units <= room
-                  ? tiles <= kTreeAlone && static_cast<double>(tiles) * (room - units) <= kTreeShort * room
-                  : !l.tc && tiles <= kTreeAloneMany && units <= 0x7fffffffLL;
+                  ? blocks <= kTreeAlone && static_cast<double>(blocks) * (room - units) <= kTreeShort * room
+                  : !l.tc && blocks <= kTreeAloneMany && units <= 0x7fffffffLL;
   if (l.by_unit) {
     l.grid = static_cast<int>(units);
   } else {

@@ -28,15 +28,29 @@ struct Row16 {
   uint4 a, b;  // 16 bf16
 };
 
-// Largest finite |x| of the 16 values, as bf16 bits (0 when there is none).
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Largest finite |x| of the 16 values, as bf16 bits (0 when there is none). Magnitudes
+// are ordered as their bits are, so two at a time are compared as 16-bit integers; only
+// a row with infinities or NaN among them is looked at value by value.
 __device__ __forceinline__ uint32_t finite_max(const Row16& r) {
   const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-  uint32_t m = 0;
+  uint32_t two = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-    m = max(m, lo < 0x7f80u ? lo : 0u);
-    m = max(m, hi < 0x7f80u ? hi : 0u);
+  for (int i = 0; i < 8; ++i) two = max_u16x2(two, w[i] & 0x7fff7fffu);
+  uint32_t m = max(two & 0xffffu, two >> 16);
+  if (m >= 0x7f80u) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+      m = max(m, lo < 0x7f80u ? lo : 0u);
+      m = max(m, hi < 0x7f80u ? hi : 0u);
+    }
   }
   return m;
 }
@@ -50,11 +64,17 @@ __device__ __forceinline__ int scale_exponent(uint32_t amax) {
   return min(max(e, -117), 119);
 }
 
-__device__ __forceinline__ uint32_t quantise4(uint32_t lo, uint32_t hi, float inv) {
-  const float2 x = unpack_bf16x2(lo), y = unpack_bf16x2(hi);
-  uint16_t a, b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x.y * inv), "f"(x.x * inv));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(y.y * inv), "f"(y.x * inv));
+__device__ __forceinline__ uint16_t quantise2(uint32_t two, uint64_t inv) {
+  const float2 x = unpack_bf16x2(two);
+  float lo, hi;
+  f2_unpack(mul2(f2_pack(x.x, x.y), inv), lo, hi);
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t quantise4(uint32_t lo, uint32_t hi, uint64_t inv) {
+  const uint16_t a = quantise2(lo, inv), b = quantise2(hi, inv);
   return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
 }
 
@@ -66,7 +86,8 @@ __device__ __forceinline__ void write_row(const Row16& r, unsigned char* cache, 
 #pragma unroll
   for (int o = T / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   const int e = scale_exponent(m);
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, a normal number
+  const float back = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, a normal number
+  const uint64_t inv = f2_pack(back, back);
   if (!live) return;
   uint4 c;
   c.x = quantise4(r.a.x, r.a.y, inv);

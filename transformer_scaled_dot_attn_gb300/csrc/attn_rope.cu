@@ -147,25 +147,23 @@ __device__ __forceinline__ float row_sum(float s) {
   return s;
 }
 
-// A thread's columns: two chunks of eight.
+// A thread's columns: two chunks of eight, one in each half of the turned columns,
+// or of the others. (Neighbouring threads' chunks are neighbours, so that a warp's
+// access takes whole 32-byte sectors: with chunks side by side in the threads of columns
+// that are not turned, the gradients of 96 x 256 tokens, 8 + 8 heads, half of 64 columns
+// turned, took 38 us instead of 32.)
 struct Columns {
-  int c0, c1, pair0;             // first columns of the chunks, first column pair
+  int c0, c1;                    // first columns of the chunks
+  int pair0, pair1;              // first column pair of the first four, of the other four
   bool turned;
 
-  __device__ __forceinline__ void init(const NormRopeParams& p, int tau) {
+  __device__ __forceinline__ void init(const NormRopeParams& p, int d, int tau) {
     const int tr = p.rot / 16;   // threads of a row whose columns are turned
     turned = tau < tr;
-    pair0 = tau * 8;
-    if (!turned) {
-      c0 = p.rot + (tau - tr) * 16;
-      c1 = c0 + 8;
-    } else if (p.interleaved) {
-      c0 = tau * 16;
-      c1 = c0 + 8;
-    } else {
-      c0 = tau * 8;
-      c1 = c0 + p.rot / 2;
-    }
+    c0 = turned ? tau * 8 : p.rot + (tau - tr) * 8;
+    c1 = c0 + (turned ? p.rot : d - p.rot) / 2;
+    pair0 = p.interleaved ? c0 / 2 : c0;
+    pair1 = p.interleaved ? c1 / 2 : c0 + 4;
   }
 };
 
@@ -190,7 +188,7 @@ __device__ __forceinline__ void angles(const NormRopeParams& p, const Columns& c
     float x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int pair = c.pair0 + 2 * j + e;
+      const int pair = (j < 2 ? c.pair0 : c.pair1) + 2 * (j & 1) + e;
       const int at = pair < p.sec0 ? pos[0] : pair < p.sec1 ? pos[1] : pos[2];
       const unsigned long long t = rates[pair] * static_cast<unsigned long long>(static_cast<long long>(at));
       const int q = static_cast<int>((t + 0x80000000ull) >> 32);  // nearest 2^-32 of a turn, in [-1/2, 1/2)
@@ -216,7 +214,7 @@ __global__ void __launch_bounds__(kNrThreads, 3) attn_norm_rope_kernel(const Nor
   const unsigned b = static_cast<unsigned>(tk) / static_cast<unsigned>(p.n);  // (B n < 2^31)
   const unsigned i = static_cast<unsigned>(tk) - b * static_cast<unsigned>(p.n);
   Columns col;
-  col.init(p, tau);
+  col.init(p, D, tau);
   fill_rates(p, rates);
   uint64_t cs[4], sn[4], ns[4];
   angles(p, col, rates, tk, cs, sn, ns);
@@ -287,7 +285,7 @@ __global__ void __launch_bounds__(kNrThreads, 2) attn_norm_rope_bwd_kernel(const
   const int tau = threadIdx.x % T, grp = threadIdx.x / T;
   grid_launch_dependents();
   Columns col;
-  col.init(p, tau);
+  col.init(p, D, tau);
   fill_rates(p, rates);
   const bool is_q = static_cast<int>(blockIdx.y) < p.q_chunks;
   const int heads = is_q ? p.h : p.h_kv;

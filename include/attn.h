@@ -435,7 +435,11 @@ int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_exp,
  *        be NULL when that is 0; every byte read is written first; not shared by
  *        calls that can overlap)
  * Scores, sums and O accumulate in fp32; the weights are rounded to bf16 for
- * the product with V. d in {32, 64, 128}, h a multiple of h_kv.
+ * the product with V. e4m3 caches multiply in f16: codes exactly, queries to 2^-39
+ * of a row's largest element, weights (times their key's scale relative to the
+ * largest met) rounded to f16; where a key head has many query rows, the elements of
+ * keys and values are held to 2^-32 of the largest scale that a CTA's keys have,
+ * so exactly from 2^-22 of it on. d in {32, 64, 128}, h a multiple of h_kv.
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG (null or misaligned pointer, n outside
  * [1, 64], m < 1, h not a multiple of h_kv, short workspace, non-finite scale),
  * ATTN_ERR_UNSUPPORTED (other d, B h_kv > 65535, h n >= 2^20) or ATTN_ERR_CUDA.

@@ -163,6 +163,56 @@ def test_row_counts_in_large_batches(n, d):
 
 
 @pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("n,group", [(64, 1), (40, 4), (64, 8)])
+def test_short_sequences_of_many_scales(n, group, d, quantised):
+    """A thousand (sequence, head)s of one or two key tiles, which differ in scale by up to 2^24:
+    nothing of one may be taken for another's. Some hold a NaN value that some of their
+    queries see."""
+    B, hkv, m, most = 128, 8, 3500, 170
+    g = torch.Generator().manual_seed(n + d)
+    lens = [64 + int(torch.randint(0, 100, (1,), generator=g)) for _ in range(B)]
+    q = R.bf16(B, hkv * group, n, d, seed=n)
+    k, v = R.bf16(B, hkv, most, d, seed=1), R.bf16(B, hkv, most, d, seed=2)
+    k, v = ((x.float() * torch.exp2(torch.randint(lo, hi, (B, hkv, 1, 1), generator=g).float())).bfloat16()
+            for x, lo, hi in ((k, -12, 1), (v, -12, 13)))
+    words = R.random_tree(B, n, n)
+    bad = torch.rand(B, hkv, generator=g) < 0.3
+
+    def cache(x):
+        c = torch.zeros(B, hkv, m, *x.shape[3:], dtype=torch.uint8 if quantised else torch.bfloat16, device=DEV)
+        c[:, :, :most] = x.to(DEV)
+        return c
+
+    if quantised:
+        (kc, ke), (vc, ve) = R.quantise(k), R.quantise(v)
+        c = [cache(x.float().to(E4M3).view(torch.uint8)) for x in (kc, vc)] + [cache(ke), cache(ve)]
+        k, v = (x * torch.exp2(e.double() - 127)[..., None] for x, e in ((kc, ke), (vc, ve)))
+    else:
+        c = [cache(k), cache(v), None, None]
+    for b in range(B):
+        for h in range(hkv):
+            if bad[b, h]:
+                c[1][b, h, lens[b] - n + 5, 7] = 0x7f if quantised else float("nan")
+    if quantised:
+        c[:2] = [x.view(E4M3) for x in c[:2]]
+    o, lse = run(q, c, lens, words, d ** -0.5)
+    o, lse = o.cpu(), lse.cpu()
+    nan = torch.isnan(o)
+    sees5 = torch.tensor([[bool(w >> 5 & 1) for w in r] for r in words])
+    assert torch.equal(nan[..., 7], (sees5[:, None] & bad[..., None]).repeat_interleave(group, 1))
+    assert not nan[..., torch.arange(d) != 7].any()
+    for b in range(B):
+        h = b % hkv
+        hs = slice(h * group, (h + 1) * group)
+        ref = list(R.tree_step(q[b:b + 1, hs], k[b:b + 1, h:h + 1], v[b:b + 1, h:h + 1], [lens[b]], [words[b]], d ** -0.5))
+        got = o[b:b + 1, hs].clone()
+        got[nan[b:b + 1, hs]] = 0
+        ref[0][nan[b:b + 1, hs]] = 0
+        R.check_tree(got, lse[b:b + 1, hs], ref)
+
+
+@pytest.mark.parametrize("quantised", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 def test_scores_that_grow_along_the_cache(d, quantised):
     """A running maximum that has to move many times: keys longer from tile to tile, and back."""

@@ -176,3 +176,14 @@ def test_binding_checks_tensors(lib):
         A.attn_decode_tree(torch.zeros(1, 4, 3, 32, **bf), cache, cache)
     with pytest.raises(ValueError, match="workspace"):
         A.attn_decode_tree(q, cache, cache, workspace=torch.zeros(4))
+    for call, name in ((lambda: A.attn_qk_norm_rope(q, k, w, w, None, freqs), "positions"),
+                       (lambda: A.attn_qk_norm_rope(q, k, w, w, pos, 1.0), "freqs"),
+                       (lambda: A.attn_qk_norm_rope(None, None, w, w), "k"),
+                       (lambda: A.attn_cache_write(None, k, cache, cache), "k"),
+                       (lambda: A.attn_cache_write(k, None, cache, cache), "v"),
+                       (lambda: A.attn_decode_tree(None, cache, cache), "q"),
+                       (lambda: A.attn_decode_tree(q, cache, None), "v cache")):
+        with pytest.raises(TypeError, match=name):
+            call()
+    with pytest.raises(ValueError, match="dimensions"):
+        A.attn_decode_tree(q[0], cache, cache)

@@ -658,6 +658,16 @@ def _operand(name, t, shape, dtype, device):
     _refuse(name, t, shape, dtype, device)
 
 
+def _shape(name, t, dims):
+    """The shape of a tensor that has to have so many dimensions."""
+    shape = getattr(t, "shape", None)
+    if shape is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(shape)}")
+    return shape
+
+
 def _first(name, t, dims, dtype):
     """Checks the tensor that gives a call its sizes; returns its device and shape."""
     try:
@@ -708,7 +718,7 @@ def _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections):
     bf = torch.bfloat16
     first = k if q is None else q
     dev, (B, h, n, d) = _first("k" if q is None else "q", first, 4, bf)
-    h_kv = 0 if k is None else int(k.shape[1]) if k.dim() == 4 else -1
+    h_kv = 0 if k is None else _shape("k", k, 4)[1]
     if q is None:
         h = 0
     ptrs = [None if q is None else q.data_ptr(),
@@ -718,12 +728,11 @@ def _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections):
     rot, axes = 0, 1
     pos = frq = None
     if freqs is not None:
-        if freqs.dim() != 1:
-            raise ValueError("freqs must have one dimension")
-        rot = 2 * freqs.shape[0]
+        rot = 2 * _shape("freqs", freqs, 1)[0]
         frq = _operand("freqs", freqs, freqs.shape, torch.float32, dev)
-        axes = positions.shape[0] if positions.dim() == 3 else 1
-        pos = _operand("positions", positions, (axes, B, n) if positions.dim() == 3 else (B, n), torch.int32, dev)
+        several = len(getattr(positions, "shape", ())) == 3
+        axes = positions.shape[0] if several else 1
+        pos = _operand("positions", positions, (axes, B, n) if several else (B, n), torch.int32, dev)
     if sections is None:
         sec = None
         if axes > 1:
@@ -815,9 +824,7 @@ def attn_cache_write(k, v, k_cache, v_cache, kv_len=None, new_len=None, k_exp=No
     caches stays as it was. Returns (k_cache, v_cache)."""
     torch = _torch or _lookup()
     dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k_cache, v_cache, k_exp, v_exp)
-    if k.dim() != 4:
-        raise ValueError("k, v must be [B, h_kv, n, d]")
-    n = k.shape[2]
+    n = _shape("k", k, 4)[2]
     pk = _operand("k", k, (B, h_kv, n, d), torch.bfloat16, dev)
     pv = _operand("v", v, (B, h_kv, n, d), torch.bfloat16, dev)
     lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
@@ -861,9 +868,7 @@ def attn_decode_tree(q, k, v, kv_len=None, tree=None, k_exp=None, v_exp=None, sc
     torch = _torch or _lookup()
     bf = torch.bfloat16
     dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k, v, k_exp, v_exp)
-    if q.dim() != 4:
-        raise ValueError("q must be [B, h, n, d]")
-    h, n = q.shape[1], q.shape[2]
+    _, h, n, _ = _shape("q", q, 4)
     pq = _operand("q", q, (B, h, n, d), bf, dev)
     lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
     words = None if tree is None else _operand("tree", tree, (B, n), torch.int64, dev)

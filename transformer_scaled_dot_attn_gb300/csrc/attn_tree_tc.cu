@@ -104,6 +104,11 @@ struct Tc {
 
 constexpr int kMaxRing = 6;
 
+// Parts whose facts are kept: the loads of a part wait for the scores of the one
+// before, which are at most two parts ahead of the weights, so whoever is ahead of
+// the softmax has begun at most four parts more.
+constexpr int kParts = 8;
+
 struct TcShared {
   uint64_t q_full, q_empty;                    // TMA; released by the part's last scores
   uint64_t q_ready[2];                         // a query tile is there (e4m3: in f16) [issuer]
@@ -118,9 +123,9 @@ struct TcShared {
   uint64_t drain[2];                           // by issuer
   uint32_t tmem_base;
   int abort_flag;
-  int ref[4][2];                               // e4m3: largest scale byte of K and V, by part
-  int scan[4][2][4];                           // the converter warps' maxima, by part
-  int odd[4];                                  // part + 1 whose newest positions hold values that are not finite
+  int ref[kParts][2];                          // e4m3: largest scale byte of K and V, by part
+  int scan[kParts][2][4];                      // the converter warps' maxima, by part
+  int odd[kParts];                             // part + 1 whose newest positions hold values that are not finite
 };
 
 // ---------------------------------------------------------------- the pair
@@ -372,10 +377,10 @@ __device__ __forceinline__ float value_of(const TreeParams& p, int bh, int key, 
 // Reports (to both CTAs of a pair) that part `seg` holds values that are not finite among its newest positions.
 template <bool PAIR>
 __device__ __forceinline__ void mark_odd(TcShared& sh, int seg, uint32_t rank) {
-  *static_cast<volatile int*>(&sh.odd[seg & 3]) = seg + 1;
+  *static_cast<volatile int*>(&sh.odd[seg % kParts]) = seg + 1;
   if (PAIR)
     asm volatile("st.shared::cluster.u32 [%0], %1;\n\tfence.acq_rel.cluster;" ::"r"(
-                     in_cta(&sh.odd[seg & 3], rank ^ 1u)),
+                     in_cta(&sh.odd[seg % kParts], rank ^ 1u)),
                  "r"(seg + 1)
                  : "memory");
 }
@@ -422,7 +427,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       mbar_init(&sh.o_free[lane], 4 * C::CTAS);
       mbar_init(&sh.drain[lane], 1);
     }
-    if (lane < 4) sh.odd[lane] = 0;
+    if (lane < kParts) sh.odd[lane] = 0;
     if (lane == 0) {
       mbar_init(&sh.q_full, 1);
       mbar_init(&sh.q_empty, 1);
@@ -499,7 +504,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (!ok) break;
         tc_fence_after();
         if (Q8 && j == 0) {  // the part's largest K scale is known by now
-          c = fmaxf(c * pow2_of_byte(sh.ref[seg & 3][0]) * 0x1p-7f, 1e-37f);
+          c = fmaxf(c * pow2_of_byte(sh.ref[seg % kParts][0]) * 0x1p-7f, 1e-37f);
           c2 = f2_pack(c, c);
         }
         if (idle) {
@@ -599,8 +604,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (!ok) break;
       tc_fence_after();
       if (!idle) {
-        const bool odd = *static_cast<volatile int*>(&sh.odd[seg & 3]) == seg + 1;
-        const float unit_v = Q8 ? pow2_of_byte(sh.ref[seg & 3][1]) * 0x1p-7f : 1.f;
+        const bool odd = *static_cast<volatile int*>(&sh.odd[seg % kParts]) == seg + 1;
+        const float unit_v = Q8 ? pow2_of_byte(sh.ref[seg % kParts][1]) * 0x1p-7f : 1.f;
         // the reference of l and O (only NaN scores: 0)
         m_used = m_used == -INFINITY ? (l != 0.f ? 0.f : -INFINITY) : m_used - kLow;
         const float inv = m_used == -INFINITY ? 0.f : unit_v / l;
@@ -684,7 +689,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       for (int kind = 0; kind < 2; ++kind) {
         if (kind < first_kind || kind > last_kind) continue;
         const unsigned all = __reduce_max_sync(0xffffffffu, most[kind]);
-        if (lane == 0) sh.scan[seg & 3][kind][warp & 3] = static_cast<int>(all);
+        if (lane == 0) sh.scan[seg % kParts][kind][warp & 3] = static_cast<int>(all);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(scanned);
@@ -692,10 +697,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       if (!ok) break;
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {
-        const int* of = sh.scan[seg & 3][kind];
+        const int* of = sh.scan[seg % kParts][kind];
         if (kind < first_kind || kind > last_kind) continue;
         top[kind] = max(max(of[0], of[1]), max(of[2], of[3]));
-        if (t == 0) sh.ref[seg & 3][kind] = top[kind];
+        if (t == 0) sh.ref[seg % kParts][kind] = top[kind];
       }
 #pragma unroll 1
       for (int x = 0; ok && x < T + last_kind; ++x) {

@@ -263,6 +263,30 @@ def test_same_bits_from_any_workspace_and_stream(quantised):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+def test_allocations_belong_to_the_stream_of_the_call():
+    """What a call on another stream allocates is not handed out again on this one while the
+    call is still waiting to run."""
+    B, h, hkv, n, m, d = 2, 4, 2, 20, 3000, 128
+    q = R.bf16(B, h, n, d, seed=1).to(DEV)
+    c, _ = caches(B, hkv, m, d, False, 2)
+    first = A.attn_decode_tree(q, c[0], c[1], scale=0.1)
+    busy = torch.ones(8192, 8192, device=DEV)
+    need = A.attn_decode_tree_workspace_bytes(B, h, hkv, n, m, d)
+    assert need > 0
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                busy @ busy
+        again = A.attn_decode_tree(q, c[0], c[1], scale=0.1, stream=side)
+        junk = [torch.full((need,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        assert all(bool((x == 255).all()) for x in junk)
+        del junk, again
+
+
 def test_captured_step_follows_the_lengths():
     B, h, hkv, n, m, d = 2, 4, 2, 3, 600, 64
     q = R.bf16(B, h, n, d, seed=1)

@@ -618,7 +618,8 @@ def attn_bwd_noalloc(q, k, v, o, lse, dO, causal: bool = False, scale: Optional[
 
 # (These calls are made once or several times for every layer of a decoding step, so
 # a check that passes costs as little as it can; what a check objects to is found out
-# afterwards. torch and two of its functions are looked up once.)
+# afterwards. torch and two of its functions are looked up once. A call's own
+# allocations and its launch go to the current stream of the tensors' device.)
 _torch = _raw_stream = _current_device = None
 
 
@@ -693,23 +694,15 @@ def _workspace(t, need, device):
     return t, t.data_ptr(), t.numel() * t.element_size()
 
 
-def _launch(fn, where, device, stream, *args):
-    """Calls fn(*args, stream) with the tensors' device current; raises on a status."""
+def _elsewhere(where, device, stream):
+    """The context of a call whose tensors are not on the current device, or that was given a
+    stream: what it allocates then belongs to the stream that uses it."""
     torch = _torch or _lookup()
-    index = device.index
     if stream is None:
-        handle = _raw_stream(index)
-    elif stream.device != device:
+        return torch.cuda.device(device)
+    if stream.device != device:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
-    else:
-        handle = stream.cuda_stream
-    if _current_device() == index:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
-    if st != ATTN_OK:
-        raise AttnError(st, where)
+    return torch.cuda.stream(stream)
 
 
 def _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections):
@@ -756,6 +749,9 @@ def attn_qk_norm_rope(q, k, w_q, w_k, positions=None, freqs=None, sections=None,
     Returns (q_out, k_out)."""
     torch = _torch or _lookup()
     dev, (B, h, h_kv, n, d, rot, axes, sec), ptrs = _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections)
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere("attn_qk_norm_rope", dev, stream):
+            return attn_qk_norm_rope(q, k, w_q, w_k, positions, freqs, sections, interleaved, eps, q_out, k_out)
     if q is not None and q_out is None:
         q_out = torch.empty_like(q)
     if k is not None and k_out is None:
@@ -763,8 +759,10 @@ def attn_qk_norm_rope(q, k, w_q, w_k, positions=None, freqs=None, sections=None,
     po = None if q is None else _operand("q_out", q_out, q.shape, torch.bfloat16, dev)
     ko = None if k is None else _operand("k_out", k_out, k.shape, torch.bfloat16, dev)
     lib = _lib or load_library()
-    _launch(lib.attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, *ptrs, po, ko, B, h, h_kv, n, d, rot, axes, sec,
-            1 if interleaved else 0, eps)
+    st = lib.attn_qk_norm_rope(*ptrs, po, ko, B, h, h_kv, n, d, rot, axes, sec, 1 if interleaved else 0, eps,
+                               _raw_stream(dev.index))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_qk_norm_rope")
     return q_out, k_out
 
 
@@ -780,6 +778,10 @@ def attn_qk_norm_rope_bwd(q, k, w_q, w_k, positions, freqs, dq_out, dk_out, sect
     torch = _torch or _lookup()
     bf = torch.bfloat16
     dev, (B, h, h_kv, n, d, rot, axes, sec), ptrs = _norm_rope_args(q, k, w_q, w_k, positions, freqs, sections)
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere("attn_qk_norm_rope_bwd", dev, stream):
+            return attn_qk_norm_rope_bwd(q, k, w_q, w_k, positions, freqs, dq_out, dk_out, sections, interleaved, eps,
+                                         dq, dk, dw_q, dw_k, workspace)
     up, out, dws = [], [], []
     if q is not None:
         dq = torch.empty_like(q) if dq is None else dq
@@ -794,8 +796,10 @@ def attn_qk_norm_rope_bwd(q, k, w_q, w_k, positions, freqs, dq_out, dk_out, sect
     lib = _lib or load_library()
     need = 0 if workspace is not None else lib.attn_qk_norm_rope_bwd_workspace_bytes(B, h, h_kv, n, d)
     workspace, ws, ws_bytes = _workspace(workspace, need, dev)
-    _launch(lib.attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream, *ptrs, *up, *out, *dws, B, h, h_kv, n, d,
-            rot, axes, sec, 1 if interleaved else 0, eps, ws, ws_bytes)
+    st = lib.attn_qk_norm_rope_bwd(*ptrs, *up, *out, *dws, B, h, h_kv, n, d, rot, axes, sec, 1 if interleaved else 0,
+                                   eps, ws, ws_bytes, _raw_stream(dev.index))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dw_q, dw_k
 
 
@@ -824,13 +828,18 @@ def attn_cache_write(k, v, k_cache, v_cache, kv_len=None, new_len=None, k_exp=No
     caches stays as it was. Returns (k_cache, v_cache)."""
     torch = _torch or _lookup()
     dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k_cache, v_cache, k_exp, v_exp)
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere("attn_cache_write", dev, stream):
+            return attn_cache_write(k, v, k_cache, v_cache, kv_len, new_len, k_exp, v_exp)
     n = _shape("k", k, 4)[2]
     pk = _operand("k", k, (B, h_kv, n, d), torch.bfloat16, dev)
     pv = _operand("v", v, (B, h_kv, n, d), torch.bfloat16, dev)
     lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
     new = None if new_len is None else _operand("new_len", new_len, (B,), torch.int32, dev)
     lib = _lib or load_library()
-    _launch(lib.attn_cache_write, "attn_cache_write", dev, stream, pk, pv, kc, vc, ke, ve, lens, new, B, h_kv, n, m, d)
+    st = lib.attn_cache_write(pk, pv, kc, vc, ke, ve, lens, new, B, h_kv, n, m, d, _raw_stream(dev.index))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_write")
     return k_cache, v_cache
 
 
@@ -841,13 +850,18 @@ def attn_cache_read(k_cache, v_cache, k_exp, v_exp, kv_len=None, k=None, v=None,
     if k_exp is None:
         raise ValueError("attn_cache_read takes a quantised cache: k_exp and v_exp are needed")
     dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k_cache, v_cache, k_exp, v_exp)
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere("attn_cache_read", dev, stream):
+            return attn_cache_read(k_cache, v_cache, k_exp, v_exp, kv_len, k, v)
     k = torch.empty(k_cache.shape, dtype=torch.bfloat16, device=dev) if k is None else k
     v = torch.empty(k_cache.shape, dtype=torch.bfloat16, device=dev) if v is None else v
     pk = _operand("k", k, k_cache.shape, torch.bfloat16, dev)
     pv = _operand("v", v, k_cache.shape, torch.bfloat16, dev)
     lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
     lib = _lib or load_library()
-    _launch(lib.attn_cache_read, "attn_cache_read", dev, stream, kc, vc, ke, ve, pk, pv, lens, B, h_kv, m, d)
+    st = lib.attn_cache_read(kc, vc, ke, ve, pk, pv, lens, B, h_kv, m, d, _raw_stream(dev.index))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_read")
     return k, v
 
 
@@ -868,6 +882,9 @@ def attn_decode_tree(q, k, v, kv_len=None, tree=None, k_exp=None, v_exp=None, sc
     torch = _torch or _lookup()
     bf = torch.bfloat16
     dev, (B, h_kv, m, d), (kc, vc, ke, ve) = _cache_args(k, v, k_exp, v_exp)
+    if stream is not None or _current_device() != dev.index:
+        with _elsewhere("attn_decode_tree", dev, stream):
+            return attn_decode_tree(q, k, v, kv_len, tree, k_exp, v_exp, scale, out, lse, need_lse, workspace)
     _, h, n, _ = _shape("q", q, 4)
     pq = _operand("q", q, (B, h, n, d), bf, dev)
     lens = None if kv_len is None else _operand("kv_len", kv_len, (B,), torch.int32, dev)
@@ -880,6 +897,9 @@ def attn_decode_tree(q, k, v, kv_len=None, tree=None, k_exp=None, v_exp=None, sc
     lib = _lib or load_library()
     need = 0 if workspace is not None else lib.attn_decode_tree_workspace_bytes(B, h, h_kv, n, m, d)
     workspace, ws, ws_bytes = _workspace(workspace, need, dev)
-    _launch(lib.attn_decode_tree, "attn_decode_tree", dev, stream, pq, kc, vc, po, pl, ke, ve, lens, words, B, h, h_kv,
-            n, m, d, 1.0 / math.sqrt(d) if scale is None else float(scale), ws, ws_bytes)
+    st = lib.attn_decode_tree(pq, kc, vc, po, pl, ke, ve, lens, words, B, h, h_kv, n, m, d,
+                              1.0 / math.sqrt(d) if scale is None else float(scale), ws, ws_bytes,
+                              _raw_stream(dev.index))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_decode_tree")
     return out, lse

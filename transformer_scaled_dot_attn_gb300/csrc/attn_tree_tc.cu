@@ -11,7 +11,7 @@
 //   512 rows: a pair with two query tiles in each CTA, which take turns: while one
 //     tile's scores are exponentiated, the tensor cores have the other's products.
 // Bound by that exchange. 4 sequences of 20480 positions, 4 key heads of 512 rows,
-// d = 128: 75 us over bf16 caches, 81 over e4m3 (the products alone need 44.5 at
+// d = 128: 71 us over bf16 caches, 81 over e4m3 (the products alone need 44.5 at
 // the rate of a large matrix product); a pair with one tile took 81 and 96. A turn
 // of the two tiles takes some 2800 clocks, 2180 of them products, and a share of
 // 34 turns starts with 10 us of first loads and set-up.
@@ -555,21 +555,27 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             tmem_st16(t_s + q * 16, pk);
           }
         };
-        refer();
-        weights(0);
-        float mx[4];
+        // (The second time in a loop over bf16 caches, so that the code of the first
+        // tile, whose weights are always taken again, is there already: 71.9 us for
+        // 74.0 of the case above. Over e4m3 caches, whose softmax warps share the
+        // issue slots with the converters, as code of its own: 81.5 for 86.1.)
+#pragma unroll 1
+        while (true) {
+          refer();
+          weights(0);
+          float mx[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) mx[v] = fmaxf(__uint_as_float(s[0][2 * v]), __uint_as_float(s[0][2 * v + 1]));
+          for (int v = 0; v < 4; ++v) mx[v] = fmaxf(__uint_as_float(s[0][2 * v]), __uint_as_float(s[0][2 * v + 1]));
 #pragma unroll
-        for (int e = 8; e < kBN; e += 8)
+          for (int e = 8; e < kBN; e += 8)
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            mx[v] = max3(mx[v], __uint_as_float(s[(e + 2 * v) >> 5][(e + 2 * v) & 31]),
-                         __uint_as_float(s[(e + 2 * v + 1) >> 5][(e + 2 * v + 1) & 31]));
-        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        const bool moved = m_new > m_used + kGrow;
-        tmem_st_wait();
-        if (__any_sync(0xffffffffu, moved)) {
+            for (int v = 0; v < 4; ++v)
+              mx[v] = max3(mx[v], __uint_as_float(s[(e + 2 * v) >> 5][(e + 2 * v) & 31]),
+                           __uint_as_float(s[(e + 2 * v + 1) >> 5][(e + 2 * v + 1) & 31]));
+          const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+          const bool moved = m_new > m_used + kGrow;
+          tmem_st_wait();
+          if (!__any_sync(0xffffffffu, moved)) break;
           const float alpha = moved ? ex2_approx(m_used - m_new) : 1.f;  // from -inf: 0
           if (moved) m_used = m_new;
           if (j > 0) {
@@ -583,10 +589,14 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             tc_rescale<D>(t_o, alpha);
             l *= alpha;
           }
-          refer();
-          weights(0);
-          tmem_st_wait();
+          if (Q8) {
+            refer();
+            weights(0);
+            tmem_st_wait();
+            break;
+          }
         }
+        if (!ok) break;
         tc_fence_before();
         tell_issuer<PAIR>(&sh.p_full[u][0]);
         weights(1);

@@ -782,22 +782,22 @@ def attn_qk_norm_rope_bwd(q, k, w_q, w_k, positions, freqs, dq_out, dk_out, sect
         with _elsewhere("attn_qk_norm_rope_bwd", dev, stream):
             return attn_qk_norm_rope_bwd(q, k, w_q, w_k, positions, freqs, dq_out, dk_out, sections, interleaved, eps,
                                          dq, dk, dw_q, dw_k, workspace)
-    up, out, dws = [], [], []
+    gq = gk = pq = pk = wq = wk = None
     if q is not None:
         dq = torch.empty_like(q) if dq is None else dq
         dw_q = torch.empty_like(w_q) if dw_q is None else dw_q
+        gq, pq = _operand("dq_out", dq_out, q.shape, bf, dev), _operand("dq", dq, q.shape, bf, dev)
+        wq = _operand("dw_q", dw_q, w_q.shape, bf, dev)
     if k is not None:
         dk = torch.empty_like(k) if dk is None else dk
         dw_k = torch.empty_like(w_k) if dw_k is None else dw_k
-    for name, x, g, dx, dw in (("q", q, dq_out, dq, dw_q), ("k", k, dk_out, dk, dw_k)):
-        up.append(None if x is None else _operand(f"d{name}_out", g, x.shape, bf, dev))
-        out.append(None if x is None else _operand(f"d{name}", dx, x.shape, bf, dev))
-        dws.append(None if x is None else _operand(f"dw_{name}", dw, (d,), bf, dev))
+        gk, pk = _operand("dk_out", dk_out, k.shape, bf, dev), _operand("dk", dk, k.shape, bf, dev)
+        wk = _operand("dw_k", dw_k, w_k.shape, bf, dev)
     lib = _lib or load_library()
     need = 0 if workspace is not None else lib.attn_qk_norm_rope_bwd_workspace_bytes(B, h, h_kv, n, d)
     workspace, ws, ws_bytes = _workspace(workspace, need, dev)
-    st = lib.attn_qk_norm_rope_bwd(*ptrs, *up, *out, *dws, B, h, h_kv, n, d, rot, axes, sec, 1 if interleaved else 0,
-                                   eps, ws, ws_bytes, _raw_stream(dev.index))
+    st = lib.attn_qk_norm_rope_bwd(*ptrs, gq, gk, pq, pk, wq, wk, B, h, h_kv, n, d, rot, axes, sec,
+                                   1 if interleaved else 0, eps, ws, ws_bytes, _raw_stream(dev.index))
     if st != ATTN_OK:
         raise AttnError(st, "attn_qk_norm_rope_bwd")
     return dq, dk, dw_q, dw_k

@@ -1089,12 +1089,12 @@ void small_shape(int d, bool quantised, bool few, int* places, int* tile) {
 // 128 keys as 1, the second was measured at `tile` for 128 keys, `start` for each
 // unit it begins (e4m3: its scales are looked at first) and, where the whole step is
 // so small that latency counts, `fill` more in all. (mma.sync : tcgen05 in us; 16
-// sequences of 8192 positions, 4 key heads of d = 128, bf16: 16 rows 80 : 93, 32 rows
+// sequences of 8192 positions, 8 key heads of d = 128, bf16: 16 rows 80 : 93, 32 rows
 // 159 : 93; e4m3: 32 rows 91 : 94, 48 rows 133 : 95; 64 sequences of 1024, 64 rows,
 // bf16 129 : 76, e4m3 112 : 107; 2 of 2000, 64 rows, bf16 19 : 21, 96 rows 23 : 22.)
 bool tree_uses_tc(long long heads, int rows, int m, int d, bool quantised) {
   const double tile = d == 32 ? 2.4 : !quantised ? 1.0 : d == 64 ? 2.0 : 1.8;
-  const double start = quantised ? 20.0 : 10.0, fill = d == 32 ? 1500.0 : d == 64 ? 300.0 : 500.0;
+  const double start = quantised ? 20.0 : 10.0, fill = d == 32 ? 3000.0 : d == 64 ? 600.0 : 1000.0;
   const double tiles = (m + 127) / 128, small = (rows + kTreeRows - 1) / kTreeRows, big = (rows + 127) / 128;
   return static_cast<double>(heads) * (small * tiles - big * (tile * tiles + start)) > fill;
 }

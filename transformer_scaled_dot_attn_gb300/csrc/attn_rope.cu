@@ -473,7 +473,7 @@ cudaError_t launch_bwd_d(NormRopeParams p, cudaStream_t stream) {
   prof_end(kKindNormRope, stream);
   if (e != cudaSuccess) return e;
   prof_begin(kKindNormRope, stream);
-  e = launch_dependent(attn_norm_rope_dw_kernel<D>, dim3(D / 8, 2), dim3(1024), stream, p.part, gx * p.q_chunks,
+  e = launch_dependent(attn_norm_rope_dw_kernel<D>, dim3(D / 8, 2), dim3(1024), 0, stream, p.part, gx * p.q_chunks,
                        gx * (gy - p.q_chunks), p.dw_q, p.dw_k);
   prof_end(kKindNormRope, stream);
   return e;

@@ -21,6 +21,7 @@
 // Many rows take the tcgen05 kernel (attn_tree_tc.cu).
 #include "attn_tree.cuh"
 
+#include <algorithm>
 #include <atomic>
 
 namespace attn {
@@ -889,7 +890,8 @@ attn_tree_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 #pragma unroll
           for (int j = 0; j < C::ND; ++j) {
             uint32_t v[4];
-            ldsm4_t(av + tile_off<D, false>(i * 16 + (lane & 7) + 8 * (lane >> 4), (2 * j + ((lane >> 3) & 1)) * 16), v);
+            const int r = i * 16 + (lane & 7) + 8 * (lane >> 4);
+            ldsm4_t(av + tile_off<D, false>(r, (2 * j + ((lane >> 3) & 1)) * 16), v);
             if (tail) {
               v[0] = clean_pair(v[0], ra, rb, odd);
               v[1] = clean_pair(v[1], ra, rb, odd);
@@ -985,87 +987,171 @@ __device__ __forceinline__ UnitParts unit_parts(const TreeParams& p, const TreeL
   return UnitParts{c0, c1 - c0 + 1};
 }
 
-// Grid: x = unit, y = 8 rows of its block (a warp a row).
+// A long cache of few heads has hundreds of parts a unit: so `group` warps share a
+// row's (or 32 rows') parts, each joins every group-th of them, and the group's results
+// are joined in shared memory. (One sequence of 40000 positions, one key head of 8 rows, d =
+// 128, e4m3: 15 us; with one warp for all parts of a row 85.)
+constexpr int kMergeWarps = 16;
+
+// Grid: x = unit, y = kMergeWarps / group rows of its block (or fewer, where it has fewer).
 template <int D>
-__global__ void __launch_bounds__(256) attn_tree_merge_kernel(const TreeParams p, int bn, int grid) {
+__global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_merge_kernel(const TreeParams p, int bn, int grid,
+                                                                           int group) {
+  constexpr int PER = D / 32;
+  extern __shared__ float4 merge_smem[];  // (none where a warp has all parts: the blocks wait beside the step's)
+  float (*s_o)[D] = reinterpret_cast<float (*)[D]>(merge_smem);
+  float2* s_ml = reinterpret_cast<float2*>(s_o[kMergeWarps]);
   const TreeLine l = tree_line(p, bn, grid);
-  const int unit = blockIdx.x, lane = threadIdx.x & 31;
+  const int unit = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const UnitParts u = unit_parts(p, l, unit, bn);
   grid_wait();  // the parts are written
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (u.parts == 1) return;  // one part: its CTA wrote the results
+  const int rows = static_cast<int>(blockDim.x >> 5) / group, w = warp % group;
+  const int r = blockIdx.y * rows + warp / group;
   const int row = (unit % p.row_blocks) * p.block_rows + r;
-  if (u.parts == 1 || r >= p.block_rows || row >= p.rows) return;  // one part: its CTA wrote the results
-  const size_t step = static_cast<size_t>(p.block_rows);
-  const size_t at = (static_cast<size_t>(unit) + u.first) * step + r;
-  float M = -INFINITY;
-  for (int s = lane; s < u.parts; s += 32) M = fmaxf(M, p.part_ml[2 * (at + s * step)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  constexpr int PER = D / 32;
-  float o[PER], sum = 0.f;
+  const bool live = r < p.block_rows && row < p.rows;
+  const size_t step = static_cast<size_t>(p.block_rows), at = (static_cast<size_t>(unit) + u.first) * step + r;
+  float m = -INFINITY, sum = 0.f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  if (M != -INFINITY) {
-#pragma unroll 4
-    for (int s = 0; s < u.parts; ++s) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * (at + s * step));
-      const float w = ex2_approx(ml.x - M);  // 0 for a part without a key that the row sees
-      sum = fmaf(w, ml.y, sum);
+  const int count = live ? (u.parts - w + group - 1) / group : 0;  // parts w, w + group, ...
+  for (int base = 0; base < count; base += 32) {
+    // a lane's part: its weight against the maximum so far (0 without a key that the row sees)
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (base + lane < count) {
+      const size_t mine = at + static_cast<size_t>(w + (base + lane) * group) * step;
+      ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * mine);
+    }
+    float top = ml.x;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) o[i] = fmaf(w, p.part[(at + s * step) * D + lane + 32 * i], o[i]);
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (top > m) {
+      const float f = ex2_approx(m - top);
+      m = top;
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] *= f;
+    }
+    const float weight = m == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+    float t = weight * ml.y;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+    sum += t;
+    const int n = min(32, count - base);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float f = __shfl_sync(0xffffffffu, weight, k);
+      const float* src = p.part + (at + static_cast<size_t>(w + (base + k) * group) * step) * D + lane;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = fmaf(f, src[32 * i], o[i]);
     }
   }
-  const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+  if (group > 1) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s_o[warp][lane + 32 * i] = o[i];
+    if (lane == 0) s_ml[warp] = make_float2(m, sum);
+    __syncthreads();
+    if (w != 0) return;
+    for (int k = 1; k < group; ++k) m = fmaxf(m, s_ml[warp + k].x);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] = 0.f;
+    for (int k = 0; k < group; ++k) {
+      const float f = m == -INFINITY ? 0.f : ex2_approx(s_ml[warp + k].x - m);
+      sum = fmaf(f, s_ml[warp + k].y, sum);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = fmaf(f, s_o[warp + k][lane + 32 * i], o[i]);
+    }
+  }
+  if (!live) return;
+  const float inv = m == -INFINITY ? 0.f : 1.f / sum;
   const size_t out = static_cast<size_t>(unit / p.row_blocks) * p.rows + row;
 #pragma unroll
   for (int i = 0; i < PER; ++i) p.o[out * D + lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
+  if (lane == 0 && p.lse != nullptr) p.lse[out] = m == -INFINITY ? -INFINITY : (m + log2f(sum)) * kTreeLn2;
 }
 
-// Grid: x = unit, y = 32 rows of its block (a lane a row); each of the 8 warps D / 8 columns.
+// Grid: x = unit, y = 32 rows of its block (a lane a row), z = as many of the eight
+// groups of D / 8 columns as the block has groups of warps.
 template <int D>
-__global__ void __launch_bounds__(256) attn_tree_tc_merge_kernel(const TreeParams p, int bn, int grid) {
+__global__ void __launch_bounds__(kMergeWarps * 32) attn_tree_tc_merge_kernel(const TreeParams p, int bn, int grid,
+                                                                              int group) {
+  constexpr int C4 = D / 32;  // groups of four columns
+  extern __shared__ float4 merge_smem[];
+  float4 (*s_o)[C4][32] = reinterpret_cast<float4 (*)[C4][32]>(merge_smem);
+  float2 (*s_ml)[32] = reinterpret_cast<float2 (*)[32]>(s_o[kMergeWarps]);
   const TreeLine l = tree_line(p, bn, grid);
   const int unit = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const UnitParts u = unit_parts(p, l, unit, bn);
   grid_wait();
+  if (u.parts == 1) return;
+  const int w = warp % group, cols = (blockIdx.z * static_cast<int>(blockDim.x >> 5) + warp) / group;
   const int r = blockIdx.y * 32 + lane;
   const int row = (unit % p.row_blocks) * p.block_rows + r;
-  if (u.parts == 1 || row >= p.rows) return;
   const size_t step = static_cast<size_t>(p.block_rows), slot = static_cast<size_t>(unit) + u.first;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + slot * step + r;
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int s = 0; s < u.parts; ++s) M = fmaxf(M, ml[s * step].x);
-  constexpr int C4 = D / 32;  // groups of four columns
+  float M = -INFINITY, sum = 0.f;
   float4 o[C4];
-  float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < C4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M != -INFINITY) {
-    const float4* part = reinterpret_cast<const float4*>(p.part) + (slot * (D / 4) + warp * C4) * step + r;
+  if (row < p.rows) {
+#pragma unroll 4
+    for (int s = w; s < u.parts; s += group) M = fmaxf(M, ml[s * step].x);
+    if (M != -INFINITY) {
+      const float4* part = reinterpret_cast<const float4*>(p.part) + (slot * (D / 4) + cols * C4) * step + r;
 #pragma unroll 2
-    for (int s = 0; s < u.parts; ++s) {
-      const float2 x = ml[s * step];
-      const float w = ex2_approx(x.x - M);
-      sum = fmaf(w, x.y, sum);
+      for (int s = w; s < u.parts; s += group) {
+        const float2 x = ml[s * step];
+        const float f = ex2_approx(x.x - M);
+        sum = fmaf(f, x.y, sum);
 #pragma unroll
-      for (int i = 0; i < C4; ++i) {
-        const float4 v = part[(static_cast<size_t>(s) * (D / 4) + i) * step];
-        o[i].x = fmaf(w, v.x, o[i].x);
-        o[i].y = fmaf(w, v.y, o[i].y);
-        o[i].z = fmaf(w, v.z, o[i].z);
-        o[i].w = fmaf(w, v.w, o[i].w);
+        for (int i = 0; i < C4; ++i) {
+          const float4 v = part[(static_cast<size_t>(s) * (D / 4) + i) * step];
+          o[i].x = fmaf(f, v.x, o[i].x);
+          o[i].y = fmaf(f, v.y, o[i].y);
+          o[i].z = fmaf(f, v.z, o[i].z);
+          o[i].w = fmaf(f, v.w, o[i].w);
+        }
       }
     }
   }
-  const float inv = M == -INFINITY ? 0.f : 1.f / sum;
   const size_t out = static_cast<size_t>(unit / p.row_blocks) * p.rows + row;
-  uint2* dst = reinterpret_cast<uint2*>(p.o + out * D + warp * (D / 8));
+  auto write = [&](int i, const float4& x, float inv) {
+    *reinterpret_cast<uint2*>(p.o + out * D + cols * (D / 8) + i * 4) =
+        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+  };
+  if (group == 1) {
+    if (row >= p.rows) return;
+    const float inv = M == -INFINITY ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int i = 0; i < C4; ++i)
-    dst[i] = make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
-  if (warp == 0 && p.lse != nullptr) p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
+    for (int i = 0; i < C4; ++i) write(i, o[i], inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C4; ++i) s_o[warp][i][lane] = o[i];
+    s_ml[warp][lane] = make_float2(M, sum);
+    __syncthreads();
+    if (row >= p.rows) return;
+    const int first = warp - w;
+    for (int k = 0; k < group; ++k) M = fmaxf(M, s_ml[first + k][lane].x);
+    auto factor = [&](int k) { return M == -INFINITY ? 0.f : ex2_approx(s_ml[first + k][lane].x - M); };
+    sum = 0.f;
+    for (int k = 0; k < group; ++k) sum = fmaf(factor(k), s_ml[first + k][lane].y, sum);
+    const float inv = M == -INFINITY ? 0.f : 1.f / sum;
+    for (int i = w; i < C4; i += group) {  // a warp of the group joins four columns
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < group; ++k) {
+        const float f = factor(k);
+        const float4 v = s_o[first + k][i][lane];
+        x.x = fmaf(f, v.x, x.x);
+        x.y = fmaf(f, v.y, x.y);
+        x.z = fmaf(f, v.z, x.z);
+        x.w = fmaf(f, v.w, x.w);
+      }
+      write(i, x, inv);
+    }
+  }
+  if (cols == 0 && w == 0 && p.lse != nullptr)
+    p.lse[out] = M == -INFINITY ? -INFINITY : (M + log2f(sum)) * kTreeLn2;
 }
 
 // Places of the mma.sync kernels on the GPU, and keys of a CTA's tile.
@@ -1075,12 +1161,16 @@ void small_shape_of(bool few, int* places, int* tile) {
   *tile = few ? Few<D, Q8>::BN : Tree<D, Q8>::BN;
 }
 
+template <int D>
+void small_shape_d(bool quantised, bool few, int* places, int* tile) {
+  quantised ? small_shape_of<D, true>(few, places, tile) : small_shape_of<D, false>(few, places, tile);
+}
+
 void small_shape(int d, bool quantised, bool few, int* places, int* tile) {
   switch (d) {
-    case 32: return quantised ? small_shape_of<32, true>(few, places, tile) : small_shape_of<32, false>(few, places, tile);
-    case 64: return quantised ? small_shape_of<64, true>(few, places, tile) : small_shape_of<64, false>(few, places, tile);
-    default:
-      return quantised ? small_shape_of<128, true>(few, places, tile) : small_shape_of<128, false>(few, places, tile);
+    case 32: return small_shape_d<32>(quantised, few, places, tile);
+    case 64: return small_shape_d<64>(quantised, few, places, tile);
+    default: return small_shape_d<128>(quantised, few, places, tile);
   }
 }
 
@@ -1136,14 +1226,27 @@ cudaError_t launch_tree_d(bool quantised, const TreePlan& plan, const CUtensorMa
   else e = launch_small_rows<D, false>(plan.grid, tk, tv, p, stream);
   if (e != cudaSuccess || plan.by_unit) return e;
   const unsigned units = static_cast<unsigned>(p.B) * p.h_kv * p.row_blocks;
+  // Warps for the parts of a unit: as many as it has on average, a power of two, from 2
+  // on while the blocks do not fill the GPU. (4 sequences, 4 key heads of 512 rows: 1, 2, 8
+  // warps 84, 81, 92 us; 8 sequences, 8 key heads, d = 64, where it has 1.2: 1, 2 217, 222.)
+  int group = 1;
+  auto blocks = [&](int g) {
+    return static_cast<long long>(units) *
+           (plan.tc ? p.block_rows / 32 * ((g + 1) / 2) : (p.block_rows * g + kMergeWarps - 1) / kMergeWarps);
+  };
+  while (group < kMergeWarps && 2ll * units * group <= plan.grid && (group == 1 || blocks(group) < kSms)) group *= 2;
+  const int warps = group == 1 ? 8 : kMergeWarps;  // of a block
+  const size_t smem = group == 1 ? 0 : plan.tc ? kMergeWarps * 32 * (D / 2 + 8) : kMergeWarps * (D * 4 + 8);
   prof_begin(kKindTreeMerge, stream);
   if (plan.tc) {
-    e = launch_dependent(attn_tree_tc_merge_kernel<D>, dim3(units, static_cast<unsigned>(p.block_rows / 32)), dim3(256),
-                         stream, p, plan.tile, plan.grid);
+    const dim3 blocks_of(units, static_cast<unsigned>(p.block_rows / 32), static_cast<unsigned>(8 * group / warps));
+    e = launch_dependent(attn_tree_tc_merge_kernel<D>, blocks_of, dim3(warps * 32), smem, stream, p, plan.tile,
+                         plan.grid, group);
   } else {
-    const int warps = p.block_rows < 8 ? p.block_rows : 8;
-    e = launch_dependent(attn_tree_merge_kernel<D>, dim3(units, static_cast<unsigned>((p.block_rows + 7) / 8)),
-                         dim3(static_cast<unsigned>(warps * 32)), stream, p, plan.tile, plan.grid);
+    const int rows = std::min(p.block_rows, warps / group);  // of a block
+    const dim3 blocks_of(units, static_cast<unsigned>((p.block_rows + rows - 1) / rows));
+    e = launch_dependent(attn_tree_merge_kernel<D>, blocks_of, dim3(static_cast<unsigned>(rows * group * 32)), smem,
+                         stream, p, plan.tile, plan.grid, group);
   }
   prof_end(kKindTreeMerge, stream);
   return e;

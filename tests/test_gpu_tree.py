@@ -49,6 +49,12 @@ CASES = [
     (2, 32, 4, 20, 1500, 64, [1500, 900], True, 2.0),
     (1, 2, 2, 2, 9000, 128, None, False, 1.0),           # a long cache split over many CTAs
     (1, 40, 1, 4, 777, 32, [700], True, 1.0),
+    # hundreds of parts to join for few heads
+    (1, 8, 1, 1, 40011, 128, [39000], False, 1.0),
+    (1, 2, 2, 1, 60000, 32, None, False, 1.0),
+    (1, 1, 1, 64, 25000, 64, [24987], True, 1.0),
+    (1, 5, 1, 60, 30000, 64, None, True, 1.0),
+    (2, 16, 2, 64, 20000, 128, [20000, 7], True, 1.0),
 ]
 
 

@@ -312,6 +312,67 @@ def test_captured_step_follows_the_lengths():
         R.check_tree(o, lse, R.tree_step(q, k, v, new, None, d ** -0.5))
 
 
+@pytest.mark.parametrize("quantised", [False, True])
+def test_captured_layers_among_copies_and_another_stream(quantised):
+    """A step of several layers in one graph: lengths copied in, norm and rotation, cache write,
+    tree attention into the next layer's input, a cache read on another stream that joins again.
+    Replays with new inputs give the bits of eager calls."""
+    layers, B, h, hkv, n, m, d = 3, 2, 8, 2, 6, 1500, 64
+    g = torch.Generator(device=DEV).manual_seed(1)
+    dtype = E4M3 if quantised else torch.bfloat16
+    kc, vc = ([torch.zeros(B, hkv, m, d, dtype=torch.float32, device=DEV).to(dtype) for _ in range(layers)] for _ in range(2))
+    ke, ve = ([torch.full((B, hkv, m), 127, dtype=torch.uint8, device=DEV) if quantised else None for _ in range(layers)]
+              for _ in range(2))
+    w = torch.ones(d, device=DEV).bfloat16()
+    freqs = (10000.0 ** (-torch.arange(d // 2, device=DEV) / (d // 2))).float()
+    kv = [torch.randn(B, hkv, n, d, device=DEV, generator=g).bfloat16() for _ in range(2 * layers)]
+    x, given, pos = torch.zeros(B, h, n, d, device=DEV).bfloat16(), i32([n, n]), i32([list(range(n))] * B)
+    lens = torch.zeros_like(given)
+    ws = torch.empty(max(16, A.attn_decode_tree_workspace_bytes(B, h, hkv, n, m, d)), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step():
+        lens.copy_(given)
+        q = x
+        for i in range(layers):
+            qn, kn = A.attn_qk_norm_rope(q, kv[2 * i], w, w, pos, freqs)
+            A.attn_cache_write(kn, kv[2 * i + 1], kc[i], vc[i], lens, k_exp=ke[i], v_exp=ve[i])
+            back = None
+            if quantised:
+                side.wait_stream(torch.cuda.current_stream())
+                back = A.attn_cache_read(kc[i], vc[i], ke[i], ve[i], lens, stream=side)
+            q, lse = A.attn_decode_tree(qn, kc[i], vc[i], lens, k_exp=ke[i], v_exp=ve[i], workspace=ws)
+            if quantised:
+                torch.cuda.current_stream().wait_stream(side)
+        return q, lse, back
+
+    def start(seed, at):
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        x.copy_(torch.randn(B, h, n, d, device=DEV, generator=gen))
+        given.copy_(i32(at))
+        for c in kc + vc:
+            c.copy_((0.1 * torch.randn(B, hkv, m, d, device=DEV, generator=gen)).to(dtype))
+
+    start(1, [n, n])
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed, at in ((2, [1500, 40]), (3, [7, 1111]), (4, [600, 1499])):
+        start(seed, at)
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        mine = [t.clone() for t in got[:2]] + [t.clone() for t in got[2] or ()]
+        start(seed, at)
+        want = step()
+        torch.cuda.synchronize()
+        for a, b in zip(mine, list(want[:2]) + list(want[2] or ())):
+            assert torch.equal(a, b)
+    assert A.attn_get_device_status() == A.ATTN_OK
+
+
 @pytest.mark.parametrize("name", list(DECODE_WORKLOADS))
 def test_benchmark_steps_quantised(name):
     """The benchmark's decoding steps at full size over quantised caches, four heads of each checked."""

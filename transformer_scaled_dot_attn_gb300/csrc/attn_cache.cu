@@ -102,6 +102,7 @@ __device__ __forceinline__ void write_row(const Row16& r, unsigned char* cache, 
 template <int D, bool QUANT>
 __global__ void __launch_bounds__(kCacheThreads) attn_cache_write_kernel(const CacheParams p) {
   constexpr int T = D / 16;
+  grid_follow();
   const int tau = threadIdx.x % T;
   const unsigned long long row64 = static_cast<unsigned long long>(blockIdx.x) * (kCacheThreads / T) + threadIdx.x / T;
   bool live = row64 < p.rows;
@@ -168,6 +169,7 @@ __device__ __forceinline__ void read_row(const unsigned char* cache, const unsig
 template <int D>
 __global__ void __launch_bounds__(kCacheThreads) attn_cache_read_kernel(const CacheParams p) {
   constexpr int T = D / 16;
+  grid_follow();
   const int tau = threadIdx.x % T;
   const unsigned long long row64 = static_cast<unsigned long long>(blockIdx.x) * (kCacheThreads / T) + threadIdx.x / T;
   if (row64 >= p.rows) return;
@@ -184,9 +186,8 @@ cudaError_t launch_write_d(bool quantised, const CacheParams& p, cudaStream_t st
   constexpr int RB = kCacheThreads / (D / 16);
   const unsigned blocks = static_cast<unsigned>((p.rows + RB - 1) / RB);
   prof_begin(kKindCache, stream);
-  if (quantised) attn_cache_write_kernel<D, true><<<blocks, kCacheThreads, 0, stream>>>(p);
-  else attn_cache_write_kernel<D, false><<<blocks, kCacheThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const auto kernel = quantised ? attn_cache_write_kernel<D, true> : attn_cache_write_kernel<D, false>;
+  const cudaError_t e = launch_dependent(kernel, dim3(blocks), dim3(kCacheThreads), 0, stream, p);
   prof_end(kKindCache, stream);
   return e;
 }
@@ -195,8 +196,8 @@ template <int D>
 cudaError_t launch_read_d(const CacheParams& p, cudaStream_t stream) {
   constexpr int RB = kCacheThreads / (D / 16);
   prof_begin(kKindCache, stream);
-  attn_cache_read_kernel<D><<<static_cast<unsigned>((p.rows + RB - 1) / RB), kCacheThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>((p.rows + RB - 1) / RB));
+  const cudaError_t e = launch_dependent(attn_cache_read_kernel<D>, grid, dim3(kCacheThreads), 0, stream, p);
   prof_end(kKindCache, stream);
   return e;
 }

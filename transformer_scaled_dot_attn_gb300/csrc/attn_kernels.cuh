@@ -253,13 +253,24 @@ int proj_bwd_splits(int M, int N, int chunks);
 // out (bf16) = sum over splits of part[z][0 .. count), count a multiple of 8.
 cudaError_t launch_proj_reduce(const float* part, void* out, long long count, int splits, cudaStream_t stream);
 
-// Programmatic dependent launch: a kernel that joins partial results is
-// started while the one that writes them still runs (its blocks wait in
-// grid_wait until those writes are visible), which hides its launch.
+// Programmatic dependent launch: a kernel is started while the one before it still
+// runs (its blocks wait in grid_wait until that one's writes are visible), which
+// hides its launch (a cache write of 16 prompts among others 26.6 -> 23.9 us, the
+// norm's backward of the base batch 35.0 -> 33.4). Every block waits, also one
+// without work: the kernel after it may rely on the kernel before it.
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The beginning of a kernel that launch_dependent launches, before it touches memory:
+// the kernel before has completed, and the next one may be placed on the SMs. (In
+// this order, so that what the next one reads before its own wait, the lengths, is
+// no younger than this one's inputs.)
+__device__ __forceinline__ void grid_follow() {
+  grid_wait();
+  grid_launch_dependents();
+}
 
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {

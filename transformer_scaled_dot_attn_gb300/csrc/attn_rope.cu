@@ -207,6 +207,7 @@ template <int D, bool INTER>
 __global__ void __launch_bounds__(kNrThreads, 3) attn_norm_rope_kernel(const NormRopeParams p) {
   constexpr int T = D / 16, RB = kNrThreads / T;
   __shared__ unsigned long long rates[D / 2];
+  grid_follow();
   const int tau = threadIdx.x % T;
   const long long tok = static_cast<long long>(blockIdx.x) * RB + threadIdx.x / T;
   const bool live = tok < p.tokens;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kNrThreads, 2) attn_norm_rope_bwd_kernel(const
   __shared__ unsigned long long rates[D / 2];
   extern __shared__ uint4 slots[];  // [kBwdAhead][4][kNrThreads]; in the end the rows' dw
   const int tau = threadIdx.x % T, grp = threadIdx.x / T;
-  grid_launch_dependents();
+  grid_follow();
   Columns col;
   col.init(p, D, tau);
   fill_rates(p, rates);
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(1024) attn_norm_rope_dw_kernel(const float* pa
   const bool is_q = blockIdx.y == 0;
   const float* src = part + (is_q ? 0 : static_cast<size_t>(q_parts) * D);
   const int count = is_q ? q_parts : k_parts;
-  grid_wait();  // the partials are written
+  grid_follow();  // the partials are written
   float s = 0.f;
 #pragma unroll 8
   for (int i = lane; i < count; i += 128) s += src[static_cast<size_t>(i) * D + c];
@@ -440,9 +441,8 @@ cudaError_t launch_fwd_d(NormRopeParams p, cudaStream_t stream) {
   p.heads_per = per;
   prof_begin(kKindNormRope, stream);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + per - 1) / per));
-  if (p.interleaved) attn_norm_rope_kernel<D, true><<<grid, kNrThreads, 0, stream>>>(p);
-  else attn_norm_rope_kernel<D, false><<<grid, kNrThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const auto kernel = p.interleaved ? attn_norm_rope_kernel<D, true> : attn_norm_rope_kernel<D, false>;
+  const cudaError_t e = launch_dependent(kernel, grid, dim3(kNrThreads), 0, stream, p);
   prof_end(kKindNormRope, stream);
   return e;
 }
@@ -467,9 +467,8 @@ cudaError_t launch_bwd_d(NormRopeParams p, cudaStream_t stream) {
   p.q_chunks = (p.h + p.heads_per - 1) / p.heads_per;
   p.token_blocks = (p.tokens + kNrThreads / (D / 16) - 1) / (kNrThreads / (D / 16));
   prof_begin(kKindNormRope, stream);
-  if (p.interleaved) attn_norm_rope_bwd_kernel<D, true><<<dim3(gx, gy), kNrThreads, kSmem, stream>>>(p);
-  else attn_norm_rope_bwd_kernel<D, false><<<dim3(gx, gy), kNrThreads, kSmem, stream>>>(p);
-  e = cudaGetLastError();
+  const auto kernel = p.interleaved ? attn_norm_rope_bwd_kernel<D, true> : attn_norm_rope_bwd_kernel<D, false>;
+  e = launch_dependent(kernel, dim3(gx, gy), dim3(kNrThreads), kSmem, stream, p);
   prof_end(kKindNormRope, stream);
   if (e != cudaSuccess) return e;
   prof_begin(kKindNormRope, stream);

@@ -399,7 +399,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   const uint32_t rank = cta_rank<PAIR>();
   volatile int* abort_flag = &sh.abort_flag;
   const Watchdog wd = p.wd;
-  grid_launch_dependents();
+  grid_follow();
   TreeWalk walk;
   if (!tree_start(p, kBN, static_cast<int>(blockIdx.x) / C::CTAS, static_cast<int>(gridDim.x) / C::CTAS, walk))
     return;  // (both CTAs of a pair, or neither)
@@ -1045,17 +1045,19 @@ cudaError_t launch_tc(int grid, const CUtensorMap& tq, const CUtensorMap& tk, co
     ready[dev & 63].store(state, std::memory_order_relaxed);
   }
   if (state == 2) return cudaErrorInvalidConfiguration;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = C::CTAS;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C::CTAS;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid * C::CTAS));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   prof_begin(kKindTree, stream);
   e = cudaLaunchKernelEx(&cfg, attn_tree_tc_kernel<D, PAIR, NQ, Q8>, tq, tk, tv, p);
   prof_end(kKindTree, stream);

@@ -77,9 +77,9 @@ struct Tc {
   static constexpr uint32_t RAW = TILE / 2;                // a tile of codes
   // rings of K and of V, and of their codes: as many places as fit, six at most
   static constexpr uint32_t ROOM = 224u * 1024u - NQ * QTILE;
-  static constexpr int least6(uint32_t n) { return n < 6 ? static_cast<int>(n) : 6; }
-  static constexpr int NT = !Q8 ? least6(ROOM / (2 * TILE)) : D < 128 ? 4 : PAIR ? 3 : 2;
-  static constexpr int NR = !Q8 ? 1 : least6((ROOM - 2 * NT * TILE) / (2 * RAW));
+  static constexpr int at_most_six(uint32_t n) { return n < 6 ? static_cast<int>(n) : 6; }
+  static constexpr int NT = !Q8 ? at_most_six(ROOM / (2 * TILE)) : D < 128 ? 4 : PAIR ? 3 : 2;
+  static constexpr int NR = !Q8 ? 1 : at_most_six((ROOM - 2 * NT * TILE) / (2 * RAW));
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = NQ * QTILE;
   static constexpr uint32_t OFF_V = OFF_K + NT * TILE;
